@@ -499,6 +499,137 @@ CSA_API csa_status csa_cp_attn_merge(const void* outs, const float* lses, int32_
 CSA_API csa_status csa_grouped_out_proj(const void* o, int64_t R, int32_t H, int32_t G, int32_t d_g,
                                         const void* w, void* y, void* stream);
 
+/*
+ * Grouped-head (GQA) dense attention and its paged cache.  The dense layers of
+ * a hybrid stack (the limit m = 1, no overlap, every entry selected of the
+ * attention above: row t sees the tokens 0 .. t), with K/V heads shared by
+ * groups of G = H / H_kv query heads: query head h reads kv head h / G.
+ * Channel widths (d_qk, d_v): (192, 128), (128, 128) or (64, 64).
+ * 1 <= H_kv, H a multiple of H_kv, G <= 128, H <= 65535.
+ *
+ * gqa_cache (host struct; device pointers): a pool of pages shared by all
+ * sequences, head-major, so that a page of one kv head is one run of memory.
+ *   k    bf16 [n_pages, H_kv, page_size, d_qk]
+ *   v    bf16 [n_pages, H_kv, page_size, d_v]
+ *   mass fp32 [n_pages, H_kv, page_size], nullable: the accumulated attention
+ *        weight of each cached token (gqa_cache_mass, gqa_cache_evict)
+ *   page_size 16, 32, 64 or 128;  n_pages * H_kv * page_size < 2^31 - 128
+ */
+typedef struct gqa_cache {
+  void* k;
+  void* v;
+  float* mass;
+  int64_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t d_qk;
+  int32_t d_v;
+} gqa_cache;
+
+/*
+ * gqa_batch (host struct; device pointers): the sequences of a call and their
+ * chunk of new tokens.  Sequence s brings the packed rows [cu_q[s],
+ * cu_q[s+1]) and its cache holds cache_len[s] tokens WITH them, so its row i
+ * (of n) stands at position cache_len[s] - n + i.  Token p of sequence s lies
+ * in slot p % page_size of page block_table[s, p / page_size]; entries of the
+ * table past the sequence's last page are not read.  The arrays are read on
+ * the device when the call runs, so a captured call may be replayed with other
+ * contents within max_q, total_q and max_pages.  Contents out of range
+ * (descending offsets, a length beyond the table, a page outside the pool)
+ * give wrong results but no access out of range: reads of a page outside the
+ * pool see zeros, writes to one are dropped.
+ */
+typedef struct gqa_batch {
+  const int32_t* block_table; /* device int32 [n_seqs, max_pages] */
+  const int32_t* cache_len;   /* device int32 [n_seqs] */
+  const int32_t* cu_q;        /* device int32 [n_seqs + 1], cu_q[0] = 0 */
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t max_q;              /* at least the most new tokens of one sequence */
+  int32_t reserved;           /* must be 0 */
+  int64_t total_q;            /* rows of the packed arrays, >= cu_q[n_seqs], < 2^31 */
+} gqa_batch;
+
+/* Workspace bytes gqa_dense_packed (max_q = packed->max_tokens) and
+ * gqa_dense_paged need on the current device: partial softmax states of items
+ * that several CTAs share.  The buffer holds no state between calls; calls
+ * that may run at the same time need one each. */
+CSA_API size_t gqa_dense_workspace_size(int64_t max_q, int32_t H, int32_t H_kv, int32_t d_v);
+
+/*
+ * gqa_dense_packed -- causal attention over whole packed prompts.  For token t
+ * of a sequence and query head h:
+ *     l_j = scale * q[t,h] . k[j,h/G]  (j <= t),  lse = ln sum_j exp(l_j),
+ *     out[t,h] = sum_j exp(l_j - lse) v[j,h/G]
+ *   q   bf16 [total_tokens, H, d_qk];  k bf16 [total_tokens, H_kv, d_qk]
+ *   v   bf16 [total_tokens, H_kv, d_v]
+ *   out bf16 [total_tokens, H, d_v];  lse fp32 [total_tokens, H] (nullable)
+ *   packed: cu_tokens, n_seqs, max_tokens and total_tokens are used (the entry
+ *   offsets are not).  scale > 0 and finite.  Rows of out and lse behind the
+ *   last sequence are left as they were.  A sequence's own keys and values
+ *   must be finite; what another sequence holds never reaches it.
+ */
+CSA_API csa_status gqa_dense_packed(const void* q, const void* k, const void* v, const csa_packed* packed, int32_t H,
+                                    int32_t H_kv, int32_t d_qk, int32_t d_v, float scale, void* out, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gqa_dense_paged -- causal attention of a chunk of new tokens over the paged
+ * cache that holds them already (gqa_cache_append).  As gqa_dense_packed, row
+ * i of sequence s seeing the cached tokens 0 .. cache_len[s] - n + i; one new
+ * token per sequence is a decode step.  A row that sees no token (a length
+ * shorter than the chunk) gets out = 0 and lse = -inf.  Slots past a
+ * sequence's length may hold anything.
+ *   q   bf16 [total_q, H, d_qk];  out bf16 [total_q, H, d_v]
+ *   lse fp32 [total_q, H] (nullable);  H a multiple of cache->n_kv_heads
+ */
+CSA_API csa_status gqa_dense_paged(const void* q, const gqa_cache* cache, const gqa_batch* batch, int32_t H, float scale,
+                                   void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gqa_cache_append -- writes a chunk's keys and values into their slots
+ * (position cache_len[s] - n + i) and sets the slots' mass, where the cache
+ * has one, to 0.  Rows at a negative position are dropped.
+ *   k bf16 [total_q, H_kv, d_qk];  v bf16 [total_q, H_kv, d_v]
+ */
+CSA_API csa_status gqa_cache_append(const void* k, const void* v, const gqa_cache* cache, const gqa_batch* batch,
+                                    void* stream);
+
+/*
+ * gqa_cache_mass -- adds to every cached token the attention weight that the
+ * chunk's rows give it, summed over the rows and the G heads of its group:
+ *     mass[h, j] += sum_{i: position of row i >= j} sum_{g<G} exp(scale q[i,hG+g] . k[j,h] - lse[i,hG+g])
+ * with the lse of gqa_dense_paged for the same rows; a row with lse = -inf
+ * adds nothing.  The sum of a call is taken in fp32 in a fixed order.
+ *   q bf16 [total_q, H, d_qk];  lse fp32 [total_q, H];  cache->mass is updated
+ */
+CSA_API csa_status gqa_cache_mass(const void* q, const float* lse, const gqa_cache* cache, const gqa_batch* batch,
+                                  int32_t H, float scale, void* stream);
+
+/* Workspace bytes gqa_cache_evict needs. */
+CSA_API size_t gqa_cache_evict_workspace_size(int32_t n_seqs, int32_t H_kv, int32_t max_pages, int32_t page_size);
+
+/*
+ * gqa_cache_evict -- cuts caches down to `budget` tokens by accumulated weight.
+ * A sequence of L <= budget tokens keeps them all.  Otherwise each kv head on
+ * its own keeps its first n_sink and last n_recent tokens and, of those
+ * between, the budget - n_sink - n_recent of the largest mass (ties to the
+ * lower position; NaN counts as the largest).  Kept tokens (k, v and mass)
+ * are copied in ascending order to tokens 0, 1, ... of the sequence's new
+ * pages.  The caches keep no positions: keys that carry rotary positions keep
+ * those they were stored with.
+ *   batch: block_table, cache_len, n_seqs and max_pages are used
+ *   new_table int32 [n_seqs, new_max_pages], new_max_pages * page_size >=
+ *         budget: pages of the same pool that no sequence of the call reads
+ *   kept  int32 [n_seqs, H_kv, budget] (output): positions kept, ascending,
+ *         -1 padded;  new_len int32 [n_seqs] (output): min(L, budget), not
+ *         the array cache_len
+ *   n_sink, n_recent >= 0, n_sink + n_recent <= budget, budget >= 1
+ */
+CSA_API csa_status gqa_cache_evict(const gqa_cache* cache, const gqa_batch* batch, int32_t budget, int32_t n_sink,
+                                   int32_t n_recent, const int32_t* new_table, int32_t new_max_pages, int32_t* kept,
+                                   int32_t* new_len, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,6 +16,13 @@ Shapes (B sequences, Tq query rows, N entries, H heads in {16, 64}):
       [B, Tq, H, 128], lse fp32 [B, Tq, H]).
   grouped_out_proj: out bf16 [..., H, 128], w bf16 [G, d_g, (H/G)*128] ->
       y bf16 [..., G, d_g].
+  gqa_dense_packed: q bf16 [tokens, H, d_qk], k bf16 [tokens, H_kv, d_qk], v
+      bf16 [tokens, H_kv, d_v] -> (out bf16 [tokens, H, d_v], lse fp32
+      [tokens, H]); H a multiple of H_kv, (d_qk, d_v) = (192, 128), (128, 128)
+      or (64, 64).
+  gqa_dense_paged: q bf16 [new tokens, H, d_qk] over a GqaCache of pages
+      [n_pages, H_kv, page_size, d]; gqa_cache_append, gqa_cache_mass and
+      gqa_cache_evict fill it, weigh its tokens and cut it down.
 """
 from __future__ import annotations
 
@@ -30,7 +37,9 @@ __all__ = ["CsaError", "KVCache", "Window", "csa_compress", "hca_compress", "csa
            "csa_indexer_topk_workspace_size", "csa_sparse_mqa", "csa_sparse_mqa_workspace_size", "hca_dense_mqa",
            "hca_dense_mqa_workspace_size", "grouped_out_proj", "launch_count", "version", "Packed", "csa_compress_append",
            "hca_compress_append", "csa_compress_packed", "hca_compress_packed", "csa_indexer_topk_packed",
-           "csa_sparse_mqa_packed", "hca_dense_mqa_packed", "csa_indexer_topk_e2m1"]
+           "csa_sparse_mqa_packed", "hca_dense_mqa_packed", "csa_indexer_topk_e2m1", "GqaCache", "GqaBatch",
+           "gqa_dense_workspace_size", "gqa_dense_packed", "gqa_dense_paged", "gqa_cache_append", "gqa_cache_mass",
+           "gqa_cache_evict"]
 
 
 class CsaError(RuntimeError):
@@ -442,3 +451,183 @@ def hca_dense_mqa_packed(q, packed: Packed, cache: KVCache, m_prime, win_k, win_
                                   0 if workspace is None else workspace.numel(), _stream(stream))
     _check(st, "hca_dense_mqa_packed")
     return out, lse
+
+
+def _tensor(t, name, dtype, shape, device):
+    """A contiguous CUDA tensor of this type, shape (None: any size) and device; its address."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return _ptr(t)
+
+
+class _On:
+    """The device of a call's tensors, and the stream it runs on, as the current ones (outputs and scratch
+    are then allocated for that stream)."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("tensor must live on a CUDA device")
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        self.cm = None
+        if stream is not None:
+            self.cm = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.cm = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.cm is not None:
+            self.cm.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.cm is not None:
+            self.cm.__exit__(*exc)
+
+
+@dataclasses.dataclass
+class GqaCache:
+    """Pages of a grouped-head cache: k bf16 [n_pages, H_kv, page_size, d_qk], v bf16 [n_pages, H_kv, page_size,
+    d_v], and optionally the accumulated weight of every token, mass fp32 [n_pages, H_kv, page_size]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    mass: torch.Tensor | None = None
+
+    def desc(self) -> _lib.GqaCacheDesc:
+        dev = self.k.device
+        P, H, S, d = self.k.shape
+        return _lib.GqaCacheDesc(_tensor(self.k, "cache.k", torch.bfloat16, (P, H, S, d), dev),
+                                 _tensor(self.v, "cache.v", torch.bfloat16, (P, H, S, None), dev),
+                                 None if self.mass is None else
+                                 _tensor(self.mass, "cache.mass", torch.float32, (P, H, S), dev),
+                                 P, S, H, d, self.v.shape[3])
+
+
+@dataclasses.dataclass
+class GqaBatch:
+    """The sequences of a call and their new tokens (device tensors, read when the call runs): block_table int32
+    [n_seqs, max_pages], cache_len int32 [n_seqs] (tokens held, the new ones included), cu_q int32 [n_seqs + 1]
+    (offsets of the new rows), and on the host max_q (at least the most new tokens of one sequence) and total_q
+    (rows of the packed arrays)."""
+    block_table: torch.Tensor
+    cache_len: torch.Tensor
+    cu_q: torch.Tensor | None
+    max_q: int = 1
+    total_q: int = 0
+
+    def desc(self, device) -> _lib.GqaBatchDesc:
+        n, m = self.block_table.shape
+        return _lib.GqaBatchDesc(_tensor(self.block_table, "block_table", torch.int32, (n, m), device),
+                                 _tensor(self.cache_len, "cache_len", torch.int32, (n,), device),
+                                 None if self.cu_q is None else
+                                 _tensor(self.cu_q, "cu_q", torch.int32, (n + 1,), device),
+                                 n, m, self.max_q, 0, self.total_q)
+
+
+def gqa_dense_workspace_size(max_q, H, H_kv, d_v) -> int:
+    return int(_lib.load().gqa_dense_workspace_size(max_q, H, H_kv, d_v))
+
+
+def _gqa_buffers(q, d_v, max_q, H_kv, out, lse, workspace):
+    R, H, _ = q.shape
+    dev = q.device
+    if out is None:
+        out = torch.empty(R, H, d_v, dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty(R, H, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(gqa_dense_workspace_size(max_q, H, H_kv, d_v), dtype=torch.uint8, device=dev)
+    return (out, lse, workspace, _tensor(out, "out", torch.bfloat16, (R, H, d_v), dev),
+            _tensor(lse, "lse", torch.float32, (R, H), dev), _ptr(workspace))
+
+
+def gqa_dense_packed(q, k, v, packed: Packed, scale, *, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention over whole packed prompts with grouped heads: row t of a sequence sees its tokens 0 .. t,
+    query head h reads kv head h // (H / H_kv).  Returns (out, lse)."""
+    lib = _lib.load()
+    dev = q.device
+    R, H, d_qk = q.shape
+    H_kv, d_v = v.shape[1], v.shape[2]
+    with _On(dev, stream) as st:
+        qp = _tensor(q, "q", torch.bfloat16, (packed.total_tokens, H, d_qk), dev)
+        kp = _tensor(k, "k", torch.bfloat16, (R, H_kv, d_qk), dev)
+        vp = _tensor(v, "v", torch.bfloat16, (R, H_kv, d_v), dev)
+        out, lse, workspace, op, lp, wp = _gqa_buffers(q, d_v, packed.max_tokens, H_kv, out, lse, workspace)
+        pd = packed.desc()
+        _check(lib.gqa_dense_packed(qp, kp, vp, ctypes.byref(pd), H, H_kv, d_qk, d_v, scale, op, lp, wp,
+                                    workspace.numel(), st), "gqa_dense_packed")
+    return out, lse
+
+
+def gqa_dense_paged(q, cache: GqaCache, batch: GqaBatch, scale, *, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of a chunk of new tokens (one: decode) over the paged cache that holds them already.
+    Returns (out, lse)."""
+    lib = _lib.load()
+    dev = q.device
+    H, d_qk = q.shape[1], q.shape[2]
+    with _On(dev, stream) as st:
+        cd, bd = cache.desc(), batch.desc(dev)
+        if cache.k.device != dev:
+            raise ValueError(f"the cache is on {cache.k.device}, not on {dev}")
+        qp = _tensor(q, "q", torch.bfloat16, (batch.total_q, H, cd.d_qk), dev)
+        out, lse, workspace, op, lp, wp = _gqa_buffers(q, cd.d_v, batch.max_q, cd.n_kv_heads, out, lse, workspace)
+        _check(lib.gqa_dense_paged(qp, ctypes.byref(cd), ctypes.byref(bd), H, scale, op, lp, wp, workspace.numel(),
+                                   st), "gqa_dense_paged")
+    return out, lse
+
+
+def gqa_cache_append(k, v, cache: GqaCache, batch: GqaBatch, *, stream=None):
+    """Writes the new tokens' k bf16 [total_q, H_kv, d_qk] and v bf16 [total_q, H_kv, d_v] into their slots, and 0
+    into the slots' mass where the cache has one."""
+    lib = _lib.load()
+    dev = cache.k.device
+    with _On(dev, stream) as st:
+        cd, bd = cache.desc(), batch.desc(dev)
+        kp = _tensor(k, "k", torch.bfloat16, (batch.total_q, cd.n_kv_heads, cd.d_qk), dev)
+        vp = _tensor(v, "v", torch.bfloat16, (batch.total_q, cd.n_kv_heads, cd.d_v), dev)
+        _check(lib.gqa_cache_append(kp, vp, ctypes.byref(cd), ctypes.byref(bd), st), "gqa_cache_append")
+
+
+def gqa_cache_mass(q, lse, cache: GqaCache, batch: GqaBatch, scale, *, stream=None):
+    """Adds to cache.mass the attention weight the chunk's rows give every cached token, summed over the rows and
+    the heads of a group; lse is gqa_dense_paged's of the same rows.  Returns cache.mass."""
+    lib = _lib.load()
+    dev = cache.k.device
+    H = q.shape[1]
+    with _On(dev, stream) as st:
+        cd, bd = cache.desc(), batch.desc(dev)
+        qp = _tensor(q, "q", torch.bfloat16, (batch.total_q, H, cd.d_qk), dev)
+        lp = _tensor(lse, "lse", torch.float32, (batch.total_q, H), dev)
+        _check(lib.gqa_cache_mass(qp, lp, ctypes.byref(cd), ctypes.byref(bd), H, scale, st), "gqa_cache_mass")
+    return cache.mass
+
+
+def gqa_cache_evict(cache: GqaCache, batch: GqaBatch, budget, new_table, *, sink=0, recent=0, kept=None, new_len=None,
+                    workspace=None, stream=None):
+    """Cuts caches of more than ``budget`` tokens down to it: every kv head keeps its first ``sink`` and last
+    ``recent`` tokens and the heaviest (cache.mass) of those between, copied in order to the pages of new_table
+    int32 [n_seqs, pages], which no sequence of the call reads.  Returns (kept int32 [n_seqs, H_kv, budget], -1
+    padded, and new_len int32 [n_seqs])."""
+    lib = _lib.load()
+    dev = cache.k.device
+    n = batch.block_table.shape[0]
+    with _On(dev, stream) as st:
+        cd, bd = cache.desc(), batch.desc(dev)
+        tp = _tensor(new_table, "new_table", torch.int32, (n, None), dev)
+        if kept is None:
+            kept = torch.empty(n, cd.n_kv_heads, budget, dtype=torch.int32, device=dev)
+        if new_len is None:
+            new_len = torch.empty(n, dtype=torch.int32, device=dev)
+        kp = _tensor(kept, "kept", torch.int32, (n, cd.n_kv_heads, budget), dev)
+        np_ = _tensor(new_len, "new_len", torch.int32, (n,), dev)
+        if workspace is None:
+            need = lib.gqa_cache_evict_workspace_size(n, cd.n_kv_heads, bd.max_pages, cd.page_size)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _check(lib.gqa_cache_evict(ctypes.byref(cd), ctypes.byref(bd), budget, sink, recent, tp, new_table.shape[1],
+                                   kp, np_, _ptr(workspace), 0 if workspace is None else workspace.numel(), st),
+               "gqa_cache_evict")
+    return kept, new_len

@@ -60,6 +60,14 @@ SIGNATURES = {
     "csa_sparse_mqa_packed": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_i32, c_vp, c_f32, c_vp, c_vp, c_vp,
                                       c_sz, c_vp]),
     "hca_dense_mqa_packed": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_f32, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "gqa_dense_workspace_size": (c_sz, [c_i64, c_i32, c_i32, c_i32]),
+    "gqa_dense_packed": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_f32, c_vp, c_vp, c_vp, c_sz,
+                                 c_vp]),
+    "gqa_dense_paged": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_f32, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "gqa_cache_append": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "gqa_cache_mass": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_f32, c_vp]),
+    "gqa_cache_evict_workspace_size": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
+    "gqa_cache_evict": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
 }
 
 
@@ -78,6 +86,18 @@ class PackedDesc(ctypes.Structure):
 class WindowDesc(ctypes.Structure):
     """csa_window."""
     _fields_ = [("k", c_vp), ("v", c_vp), ("pos0", c_i64), ("rows", c_i64), ("len", c_i32), ("reserved", c_i32)]
+
+
+class GqaCacheDesc(ctypes.Structure):
+    """gqa_cache."""
+    _fields_ = [("k", c_vp), ("v", c_vp), ("mass", c_vp), ("n_pages", c_i64), ("page_size", c_i32),
+                ("n_kv_heads", c_i32), ("d_qk", c_i32), ("d_v", c_i32)]
+
+
+class GqaBatchDesc(ctypes.Structure):
+    """gqa_batch."""
+    _fields_ = [("block_table", c_vp), ("cache_len", c_vp), ("cu_q", c_vp), ("n_seqs", c_i32), ("max_pages", c_i32),
+                ("max_q", c_i32), ("reserved", c_i32), ("total_q", c_i64)]
 
 
 _lib = None

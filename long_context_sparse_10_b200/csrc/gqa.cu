@@ -1,0 +1,828 @@
+// Dense grouped-head (GQA) attention: whole packed prompts, and chunks of new
+// tokens (one token: decode) over a paged cache.
+//
+// For row i of a sequence at position t, head h*G + g of kv head h:
+//     l_j = scale q . k_j (j <= t),  out = sum_j exp(l_j - lse) v_j,
+//     lse = ln sum_j exp(l_j)
+// (the case m = 1, no overlap, every entry visible of the compressed
+// attention).  One tcgen05 kernel serves every length; gqa_work.cuh splits the
+// key tiles of all (sequence, kv head, row block) items evenly over the CTAs.
+//
+// Roles of a CTA (one per SM, 384 threads):
+//   warps 0-3, 4-7  softmax warpgroups, one per stream: thread = row, 128
+//                   scores read from TMEM, one pass with a running reference
+//                   and sum, probabilities written back to TMEM as bf16
+//   warp 8          TMA producer (128-byte swizzled K and V tiles, rings)
+//   warp 9          one thread issues the MMAs: S = Q K^T (both operands in
+//                   shared memory), O += P V (P from TMEM, V as it lies in
+//                   memory, channel-major for the MMA)
+//   warps 10, 11    none (they complete the warpgroup whose registers move)
+// Two streams keep the tensor core busy while the other stream is in its
+// softmax.  An item of two 128-row tiles gives one tile to each stream, and
+// both read the same K/V tile; an item of at most one tile (decode) gives its
+// even key tiles to one stream and its odd ones to the other, with their own
+// references, sums and accumulators, joined in the epilogue.
+// TMEM: S of stream 0 and 1 (128 fp32 columns each; P overlays S), O of
+// stream 0 and 1.
+//
+// The softmax reference of a row follows its running maximum lazily: O and the
+// sum are rescaled only when a tile's maximum exceeds the reference by more
+// than 2^8, so the accumulator is rarely touched; probabilities then reach at
+// most 2^8, far inside bf16 and fp32, and the normalised result is the same.
+// Sums are taken in fp32 over the unrounded probabilities; P is rounded to
+// bf16 (half a step, 2^-9 relative each) because the MMA takes 16-bit operands.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+#include "gqa_host.h"
+#include "gqa_work.cuh"
+#include "host_util.h"
+#include "tc.cuh"
+
+namespace csa {
+namespace {
+
+using gqa::Geometry;
+using gqa::kTile;
+using gqa::Seq;
+using gqa::Walk;
+
+constexpr int kThreads = 384;
+// Registers: 384 threads start with 168 each; the softmax warpgroups take 208 (a row of scores is 128 of them)
+// and the third warpgroup gives up what it does not need: 2 * 208 + 88 = 3 * 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kWgThreads = 128;
+constexpr float kRescaleLog2 = 8.f;
+
+// SINGLE: every item of the call fits one 128-row tile (decode), so one Q tile
+// is held and the space goes to more stages.
+template <int DQK, int DV, bool SINGLE>
+struct Shape {
+  static constexpr int kQc = DQK / 64, kVc = DV / 64;  // 64-channel (128-byte) column blocks
+  static constexpr int kQBytes = kTile * DQK * 2, kVBytes = kTile * DV * 2;
+  static constexpr int kQTiles = SINGLE ? 1 : 2;
+  static constexpr int kKStages = DQK == 64 ? 5 : (DQK == 128 ? 3 : 2);
+  static constexpr int kVStages = DQK == 64 ? 5 : (DQK == 128 ? (SINGLE ? 3 : 2) : (SINGLE ? 2 : 1));
+  static constexpr int kRows = kQTiles * kTile;
+  static constexpr size_t kKOff = static_cast<size_t>(kQTiles) * kQBytes;
+  static constexpr size_t kVOff = kKOff + static_cast<size_t>(kKStages) * kQBytes;
+  static constexpr size_t kMiscOff = kVOff + static_cast<size_t>(kVStages) * kVBytes;
+  static constexpr size_t kBars = 2 * kKStages + 2 * kVStages + 12;
+  // barriers | partition scratch (40 int64) | TMEM slot | (reference, sum) of stream 1
+  static constexpr size_t kStatOff = kMiscOff + 8 * kBars + 8 * 40 + 16;
+  static constexpr size_t kSmem = ((kStatOff + 15) / 16) * 16 + kWgThreads * 8 + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct Params {
+  Geometry g;
+  const int32_t* block_table;  // [n_seqs, max_pages]
+  int max_pages, page, n_pages;
+  int64_t kv_rows;             // rows of the page pool: n_pages * Hkv * page
+  int Hq;
+  float scale, scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part;  // [2 C, rows, DV] unnormalised partial outputs
+  float2* ml;   // [2 C, rows] their references (log2 units) and sums
+  int4* meta;   // [C] (flags, s, h, blk) of the CTA's first piece
+};
+
+constexpr int kMetaOwner = 1;   // the first piece ends its item and does not begin it: this CTA's merge
+constexpr int kMetaBegins = 2;  // the last piece begins its item
+constexpr int kMetaSingle = 4;  // the last piece is the first
+
+// D(TMEM) += A(TMEM, bf16 pairs) * B(shared)
+__device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// 32 columns without a wait; fence_regs() after the wait keeps uses behind it.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void fence_regs(float* v) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
+                      "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 operations in one instruction (each rounded as its scalar form).
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
+  asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %4};\nmov.b64 c, {%5, %5};\n"
+      "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n.reg .b64 a, d;\nmov.b64 a, {%2, %3};\nmov.b64 d, {%0, %1};\nadd.rn.f32x2 d, d, a;\n"
+      "mov.b64 {%0, %1}, d;\n}\n"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) { tc::bar_arrive_expect_tx(bar, bytes); }
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+}
+
+// Whether stream s works on key tile j of an item whose tiles per stream are
+// n0, n1 (two tiles of rows), or one tile of rows: even and odd key tiles.
+__device__ __forceinline__ bool active(bool one, int s, int j, int n0) { return one ? (j & 1) == s : (s == 1 || j < n0); }
+
+template <int DQK, int DV, bool PAGED, bool SINGLE>
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
+                    const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using S = Shape<DQK, DV, SINGLE>;
+  pdl_wait();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* Qs = smem;
+  uint8_t* Ks = smem + S::kKOff;
+  uint8_t* Vs = smem + S::kVOff;
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + S::kMiscOff);
+  uint64_t* kempty = kfull + S::kKStages;
+  uint64_t* vfull = kempty + S::kKStages;
+  uint64_t* vempty = vfull + S::kVStages;
+  uint64_t* qfull = vempty + S::kVStages;  // [2]
+  uint64_t* qempty = qfull + 2;            // [2]
+  uint64_t* sfull = qempty + 2;            // [2] scores of a stream are in TMEM
+  uint64_t* pfull = sfull + 2;             // [2] probabilities of a stream are in TMEM
+  uint64_t* odone = pfull + 2;             // [2] a stream's PV product is complete
+  uint64_t* oempty = odone + 2;            // [2] a stream's O has been read out
+  int64_t* scratch = reinterpret_cast<int64_t*>(oempty + 2);
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(scratch + 40);
+  float2* stat = reinterpret_cast<float2*>(smem + ((S::kStatOff + 15) / 16) * 16);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Geometry& g = p.g;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::kKStages; ++i) {
+      tc::bar_init(&kfull[i], 1);
+      tc::bar_init(&kempty[i], 1);
+    }
+    for (int i = 0; i < S::kVStages; ++i) {
+      tc::bar_init(&vfull[i], 1);
+      tc::bar_init(&vempty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::bar_init(&qfull[i], 1);
+      tc::bar_init(&qempty[i], 1);
+      tc::bar_init(&sfull[i], 1);
+      tc::bar_init(&pfull[i], 4);
+      tc::bar_init(&odone[i], 1);
+      tc::bar_init(&oempty[i], kWgThreads);
+    }
+    tc::bar_init_fence();
+  }
+  if (warp == 9) tc::tmem_alloc(tslot, 512);
+  const gqa::Share share = gqa::find_share(g, blockIdx.x, gridDim.x, scratch);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tslot;
+  const uint32_t rows_q = static_cast<uint32_t>(g.tpt * g.G);
+
+  if (warp == 8) {
+    regs_down();
+    // ===================== TMA producer =====================
+    Walk w;
+    bool healthy = true;
+    int items = 0, tk = 0, tv = 0;
+    for (bool more = w.begin(g, share); more && healthy; more = w.next(g), ++items) {
+      // queries: one or two tiles
+      if (items > 0) {
+        healthy = tc::bar_wait(&qempty[0], (items - 1) & 1) && tc::bar_wait(&qempty[1], (items - 1) & 1);
+        if (!healthy) break;
+      }
+      if (lane == 0) {
+        const int nt = w.one ? 1 : 2;
+        for (int s = 0; s < nt; ++s) {
+          bar_expect(&qfull[s], rows_q * 128u * S::kQc);
+          const int tok = w.q.row0 + w.blk * g.tpb + s * g.tpt;
+          for (int c = 0; c < S::kQc; ++c)
+            tc::tma_load_3d(Qs + s * S::kQBytes + c * (kTile * 128), &qmap, c * 64, w.h * g.G, tok, &qfull[s]);
+        }
+      }
+      __syncwarp();
+      // a tile's 128 rows: one box (prompts), or one box per page and 64-channel block
+      const int live = PAGED ? (w.q.L + p.page - 1) / p.page : 0;
+      const int ppt = PAGED ? kTile / p.page : 1;
+      auto page_row = [&](int j, int pg) -> int {  // first pool row of page pg of tile j
+        const int at = j * ppt + pg;
+        if (at >= live) return static_cast<int>(p.kv_rows);  // past the pool: filled with zeros
+        const int id = __ldg(p.block_table + static_cast<int64_t>(w.s) * p.max_pages + at);
+        if (id < 0 || id >= p.n_pages) return static_cast<int>(p.kv_rows);
+        return (id * g.Hkv + w.h) * p.page;
+      };
+      auto load_tile = [&](bool is_v, int j, int row) {
+        const int chunks = is_v ? S::kVc : S::kQc;
+        const int st = is_v ? tv % S::kVStages : tk % S::kKStages;
+        const int use = is_v ? tv / S::kVStages : tk / S::kKStages;
+        uint64_t* full = is_v ? &vfull[st] : &kfull[st];
+        uint64_t* empty = is_v ? &vempty[st] : &kempty[st];
+        uint8_t* dst = is_v ? Vs + st * S::kVBytes : Ks + st * S::kQBytes;
+        if (use > 0 && !tc::bar_wait(empty, (use - 1) & 1)) return false;
+        if (lane == 0) bar_expect(full, static_cast<uint32_t>(is_v ? S::kVBytes : S::kQBytes));
+        __syncwarp();
+        if constexpr (PAGED) {
+          // at most 3 column blocks x 8 pages: a lane each
+          const int pg = lane % ppt, c = lane / ppt;
+          const int r = __shfl_sync(0xffffffffu, row, pg);
+          if (c < chunks) tc::tma_load_2d(dst + c * (kTile * 128) + pg * p.page * 128, is_v ? &vmap : &kmap, c * 64, r, full);
+          __syncwarp();
+        } else if (lane == 0) {
+          for (int c = 0; c < chunks; ++c)
+            tc::tma_load_3d(dst + c * (kTile * 128), is_v ? &vmap : &kmap, c * 64, w.h,
+                            w.q.row0 + j * kTile, full);
+        }
+        if (is_v) ++tv; else ++tk;
+        return true;
+      };
+      // K runs one tile ahead of V, as the products use them
+      int row_cur = PAGED && lane < ppt ? page_row(w.t0, lane) : 0;
+      healthy = load_tile(false, w.t0, row_cur);
+      for (int j = w.t0; j < w.t1 && healthy; ++j) {
+        int row_next = row_cur;
+        if (j + 1 < w.t1) {
+          if (PAGED && lane < ppt) row_next = page_row(j + 1, lane);
+          healthy = load_tile(false, j + 1, row_next);
+        }
+        if (healthy) healthy = load_tile(true, j, row_cur);
+        row_cur = row_next;
+      }
+    }
+  } else if (warp == 9) {
+    regs_down();
+    // ===================== MMA issue (one thread) =====================
+    if (lane == 0) {
+      constexpr uint32_t id_qk = tc::idesc_bf16(kTile, kTile, false, false);
+      constexpr uint32_t id_pv = tc::idesc_bf16(kTile, DV, true, false);
+      const uint64_t q_desc = tc::desc_sw128(smem_u32(Qs), 16, 1024), k_desc = tc::desc_sw128(smem_u32(Ks), 16, 1024);
+      const uint64_t v_desc = tc::desc_sw128(smem_u32(Vs), kTile * 128, 1024);
+      Walk w;
+      bool healthy = true;
+      int items = 0, pairs = 0;
+      int base = 0;                 // this CTA's tiles before the item
+      int np[2] = {0, 0};           // PV products issued per stream
+      for (bool more = w.begin(g, share); more && healthy; more = w.next(g), ++items) {
+        const bool one = w.one;
+        const int n0 = one ? w.n : (w.blk * g.tpb + g.tpt + (w.q.L - w.q.nq) + kTile - 1) / kTile;
+        healthy = tc::bar_wait(&qfull[0], items & 1);
+        if (!one) {
+          healthy = healthy && tc::bar_wait(&qfull[1], pairs & 1);
+          ++pairs;
+        }
+        tc::fence_after_sync();
+        if (!healthy) break;
+        auto qk = [&](int s, int j) {
+          const int t = base + j - w.t0, st = t % S::kKStages;
+          if (!tc::bar_wait(&kfull[st], (t / S::kKStages) & 1)) return false;
+          tc::fence_after_sync();
+          const uint64_t a = q_desc + (one ? 0 : s * (S::kQBytes >> 4)), b = k_desc + st * (S::kQBytes >> 4);
+#pragma unroll
+          for (int k = 0; k < DQK / 16; ++k) {
+            const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;  // descriptors count 16-byte units
+            tc::mma_bf16_ss(tmem + s * kTile, a + o, b + o, id_qk, k != 0 ? 1u : 0u);
+          }
+          tc::mma_commit(&sfull[s]);
+          if (one || s == 1) {  // the tile's last use as K
+            tc::mma_commit(&kempty[st]);
+            if (j == w.t1 - 1) {
+              tc::mma_commit(&qempty[0]);
+              tc::mma_commit(&qempty[1]);
+            }
+          }
+          return true;
+        };
+        bool first[2] = {true, true};
+        // the first scores of each stream
+        for (int s = 0; s < 2 && healthy; ++s) {
+          const int j = one ? w.t0 + s : w.t0;
+          const int st = one ? (j & 1) : s;
+          if (j < w.t1 && active(one, st, j, n0)) healthy = qk(st, j);
+        }
+        for (int j = w.t0; j < w.t1 && healthy; ++j) {
+          const int t = base + j - w.t0, sv = t % S::kVStages;
+          const uint64_t b = v_desc + sv * (S::kVBytes >> 4);
+          for (int s = 0; s < 2 && healthy; ++s) {
+            if (!active(one, s, j, n0)) continue;
+            healthy = tc::bar_wait(&vfull[sv], (t / S::kVStages) & 1) && tc::bar_wait(&pfull[s], np[s] & 1);
+            if (first[s] && items > 0) healthy = healthy && tc::bar_wait(&oempty[s], (items - 1) & 1);
+            if (!healthy) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_bf16_ts(tmem + 2 * kTile + s * DV, tmem + s * kTile + k * 8, b + k * (2048 >> 4), id_pv,
+                          (first[s] && k == 0) ? 0u : 1u);
+            tc::mma_commit(&odone[s]);
+            first[s] = false;
+            ++np[s];
+            if (one || s == 1) tc::mma_commit(&vempty[sv]);
+            const int jn = one ? j + 2 : j + 1;
+            if (jn < w.t1 && active(one, s, jn, n0)) healthy = qk(s, jn);
+          }
+        }
+        // a stream without a tile here: its previous item's read-out is awaited all the same, so that no
+        // phase of oempty is left two behind
+        for (int s = 0; s < 2; ++s)
+          if (first[s] && items > 0 && healthy) healthy = tc::bar_wait(&oempty[s], (items - 1) & 1);
+        base += w.t1 - w.t0;
+      }
+    }
+  } else if (warp >= 10) {
+    regs_down();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    // ===================== softmax, thread = row =====================
+    const int s = warp >> 2;                 // stream
+    const int r = (warp & 3) * 32 + lane;    // row of the tile = TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + s * kTile, tO = tmem + lane_base + 2 * kTile;
+    const int rt = r / g.G, rg = r - rt * g.G;  // token of the tile, head of the group
+    const bool row_used = rt < g.tpt;
+    const float sl2 = p.scale_log2;
+    const float step = kRescaleLog2 / sl2;
+    Walk w;
+    bool healthy = true;
+    int items = 0, base = 0;
+    int ns = 0;  // this stream's tiles so far
+    int first_blk = 0, first_s = 0, first_h = 0, flags = 0;
+    for (bool more = w.begin(g, share); more; more = w.next(g), ++items) {
+      const bool one = w.one;
+      const int off = w.q.L - w.q.nq;
+      const int n0 = one ? w.n : (w.blk * g.tpb + g.tpt + off + kTile - 1) / kTile;
+      const int tok = w.blk * g.tpb + (one ? 0 : s * g.tpt) + rt;
+      const bool valid = row_used && tok < w.q.nq;
+      // keys this row sees; a row that is not one is left unmasked (nobody reads its result)
+      int lim = off + tok + 1;
+      if (!valid) lim = 0x7fffffff;
+      const bool warp_valid = __any_sync(0xffffffffu, valid);
+      float m = -INFINITY, l = 0.f;
+      int done = 0;
+      for (int j = w.t0; j < w.t1; ++j) {
+        if (!active(one, s, j, n0)) continue;
+        if (healthy) healthy = tc::bar_wait(&sfull[s], ns & 1);
+        tc::fence_after_sync();
+        const int k0 = j * kTile;
+        if (warp_valid) {
+          float v[kTile];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v + 32 * c);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) fence_regs(v + 32 * c);
+          const int vis = lim - k0;
+          if (__any_sync(0xffffffffu, vis < kTile)) {
+#pragma unroll
+            for (int i = 0; i < kTile; ++i) v[i] = i < vis ? v[i] : -INFINITY;
+          }
+          float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
+#pragma unroll
+          for (int i = 4; i < kTile; i += 4) {
+            x0 = fmaxf(x0, v[i]);
+            x1 = fmaxf(x1, v[i + 1]);
+            x2 = fmaxf(x2, v[i + 2]);
+            x3 = fmaxf(x3, v[i + 3]);
+          }
+          const float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+          if (done == 0) {
+            m = mt;
+          } else {
+            const bool need = valid && mt > m + step;
+            if (__any_sync(0xffffffffu, need)) {
+              // O and l of the rows that need it move to the new reference; the previous product has to be in
+              if (healthy) healthy = tc::bar_wait(&odone[s], (ns - 1) & 1);
+              tc::fence_after_sync();
+              const float f = need ? exp2_approx((m - mt) * sl2) : 1.f;
+              if (need) m = mt;
+              l *= f;
+#pragma unroll
+              for (int c = 0; c < DV / 16; ++c) {
+                float o[16];
+                tmem_ld16(tO + s * DV + 16 * c, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= f;
+                tmem_st16(tO + s * DV + 16 * c, o);
+              }
+              tc::tmem_wait_st();
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : -m * sl2;
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              float* e = v + 32 * c + 2 * i;
+              fma2(e[0], e[1], e[0], e[1], sl2, ref);
+              fma2(e[2], e[3], e[2], e[3], sl2, ref);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) e[u] = exp2_approx(e[u]);
+              add2(l0, l1, e[0], e[1]);
+              add2(l2, l3, e[2], e[3]);
+              pk[i] = __uint_as_float(pack_bf16x2(e[0], e[1]));
+              pk[i + 1] = __uint_as_float(pack_bf16x2(e[2], e[3]));
+            }
+            tmem_st16(tS + 16 * c, pk);
+          }
+          l += (l0 + l1) + (l2 + l3);
+          tc::tmem_wait_st();
+        }
+        // keys past the sequence's end share its last tile: their values may be anything (another sequence,
+        // a page never written), and 0 x NaN is NaN, so those rows of V become zeros
+        if (w.q.L - k0 < kTile) {
+          const int t = base + j - w.t0, sv = t % S::kVStages;
+          if (healthy) healthy = tc::bar_wait(&vfull[sv], (t / S::kVStages) & 1);
+          const int from = w.q.L - k0 > 0 ? w.q.L - k0 : 0;
+          uint8_t* vb = Vs + sv * S::kVBytes;
+          for (int i = r; i < (kTile - from) * 8 * S::kVc; i += kWgThreads) {
+            const int ch = i & 7, row = from + ((i >> 3) % (kTile - from)), c = (i >> 3) / (kTile - from);
+            *reinterpret_cast<uint4*>(vb + c * (kTile * 128) + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_async_smem();
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&pfull[s]);
+        ++ns;
+        ++done;
+      }
+      // ---- epilogue ----
+      if (done > 0) {
+        if (healthy) healthy = tc::bar_wait(&odone[s], (ns - 1) & 1);
+        tc::fence_after_sync();
+      }
+      if (items == 0) {
+        first_s = w.s;
+        first_h = w.h;
+        first_blk = w.blk;
+        if (w.t0 > 0 && w.t1 == w.n) flags |= kMetaOwner;
+      }
+      flags = (flags & kMetaOwner) | (w.t0 == 0 ? kMetaBegins : 0) | (items == 0 ? kMetaSingle : 0);
+      float fa = done > 0 ? 1.f : 0.f, fb = 0.f;
+      float mr = m == -INFINITY ? -INFINITY : m * sl2;  // log2 units
+      if (one) {
+        if (s == 1) stat[r] = make_float2(done > 0 ? mr : -INFINITY, l);
+        tc::fence_before_sync();
+        named_sync(1, 2 * kWgThreads);
+        tc::fence_after_sync();
+        const float2 other = stat[r];
+        named_sync(2, 2 * kWgThreads);  // stream 1 may write the next item's
+        if (s == 0) {
+          const float top = fmaxf(mr, other.x);
+          const float ref = top == -INFINITY ? 0.f : top;
+          fa = mr == -INFINITY ? 0.f : exp2f(mr - ref);
+          fb = other.x == -INFINITY ? 0.f : exp2f(other.x - ref);
+          l = l * fa + other.y * fb;
+          mr = top;
+        }
+      }
+      if (!(one && s == 1)) {
+        const bool whole = w.whole();
+        const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;  // NaN stays NaN
+        const int64_t grow = static_cast<int64_t>(w.q.row0 + tok) * p.Hq + w.h * g.G + rg;
+        const int64_t prow = (static_cast<int64_t>(2) * blockIdx.x + (items > 0 ? 1 : 0)) * S::kRows + s * kTile + r;
+        const bool read_a = warp_valid && (fa != 0.f || fa != fa), read_b = one && warp_valid && (fb != 0.f || fb != fb);
+        const bool any_a = __any_sync(0xffffffffu, read_a), any_b = __any_sync(0xffffffffu, read_b);
+#pragma unroll
+        for (int c = 0; c < DV / 32; ++c) {
+          float o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          if (any_a) {
+            tc::tmem_ld32(tO + s * DV + 32 * c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = read_a ? o[i] * fa : 0.f;
+          }
+          if (any_b) {
+            float o2[32];
+            tc::tmem_ld32(tO + DV + 32 * c, o2);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] += read_b ? o2[i] * fb : 0.f;
+          }
+          if (valid) {
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + grow * DV + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                    pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                    pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                    pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.part + prow * DV + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+          }
+        }
+        if (valid) {
+          if (whole) {
+            if (p.lse != nullptr) p.lse[grow] = l == 0.f ? -INFINITY : (mr + log2f(l)) * kLn2;
+          } else {
+            p.ml[prow] = make_float2(mr, l);
+          }
+        }
+        tc::fence_before_sync();
+        bar_arrive(&oempty[s]);
+        if (one) bar_arrive(&oempty[1]);
+      }
+      base += w.t1 - w.t0;
+    }
+    if (tid == 0) p.meta[blockIdx.x] = make_int4(flags, first_s, first_h, first_blk);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 9) tc::tmem_dealloc(tmem, 512);
+}
+
+// Joins the partial states of items that straddle CTAs.  Block (c, y): the
+// item that CTA c's first piece ends, rows y*8 .. y*8+7, a warp per row.  The
+// pieces are CTA c's first, every whole CTA before it, and the last piece of
+// the CTA in which the item begins; they are added in that fixed order.
+template <int DV, int ROWS>
+__global__ void __launch_bounds__(256) gqa_merge_kernel(const __grid_constant__ Params p) {
+  pdl_wait();
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int4 me = p.meta[c];
+  if (!(me.x & kMetaOwner)) return;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int tile = row / kTile, r = row % kTile;
+  const int rt = r / p.g.G, rg = r - rt * p.g.G;
+  Seq q;
+  q.load(p.g, me.y);
+  const int tok = me.w * p.g.tpb + tile * p.g.tpt + rt;
+  if (rt >= p.g.tpt || tok >= q.nq) return;
+  int begin = c - 1;  // the CTA in which the item begins
+  while (begin > 0 && !(p.meta[begin].x & kMetaBegins)) --begin;
+  const int n = c - begin + 1;
+  auto slot = [&](int i) -> int64_t {  // piece i, counted back from CTA c
+    const int b = c - i;
+    const int second = (i > 0 && !(p.meta[b].x & kMetaSingle)) ? 1 : 0;
+    return (static_cast<int64_t>(2) * b + second) * ROWS + row;
+  };
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.ml[slot(i)].x);
+  top = warp_max(top);
+  const float ref = top == -INFINITY ? 0.f : top;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float wgt = 0.f, li = 0.f;
+    int64_t at = 0;
+    if (i0 + lane < n) {
+      at = slot(i0 + lane);
+      const float2 ml = p.ml[at];
+      wgt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - ref);
+      li = ml.y * wgt;
+    }
+    const int m = min(32, n - i0);
+#pragma unroll 4
+    for (int i = 0; i < m; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, wgt, i);
+      l += __shfl_sync(0xffffffffu, li, i);
+      const int64_t a = __shfl_sync(0xffffffffu, at, i);
+      if (lane < DV / 4 && wi != 0.f) {
+        const float4 o = *reinterpret_cast<const float4*>(p.part + a * DV + 4 * lane);
+        acc.x += o.x * wi;
+        acc.y += o.y * wi;
+        acc.z += o.z * wi;
+        acc.w += o.w * wi;
+      }
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const int64_t grow = static_cast<int64_t>(q.row0 + tok) * p.Hq + me.z * p.g.G + rg;
+  if (lane < DV / 4)
+    *reinterpret_cast<uint2*>(p.out + grow * DV + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0 && p.lse != nullptr) p.lse[grow] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+}
+
+
+struct Workspace {
+  size_t part, ml, meta, bytes;
+};
+Workspace layout(int64_t max_rows, int dv) {
+  const int rows = max_rows <= kTile ? kTile : 2 * kTile;
+  const size_t slots = static_cast<size_t>(2) * num_sms() * rows;
+  Workspace w;
+  w.part = 0;
+  w.ml = slots * dv * 4;
+  w.meta = w.ml + slots * 8;
+  w.bytes = w.meta + static_cast<size_t>(num_sms()) * 16;
+  return w;
+}
+
+template <int DQK, int DV, bool PAGED, bool SINGLE>
+csa_status launch(const char* what, const Params& p, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                  int64_t max_rows, cudaStream_t s) {
+  using S = Shape<DQK, DV, SINGLE>;
+  auto kern = gqa_attn_kernel<DQK, DV, PAGED, SINGLE>;
+  if (!ensure_smem(reinterpret_cast<const void*>(kern), static_cast<int>(S::kSmem)))
+    return fail(CSA_ERR_CUDA, "%s: cannot raise the shared memory limit", what);
+  const int grid = num_sms();
+  prof_begin(s);
+  cudaError_t e = launch_pdl(kern, dim3(grid), dim3(kThreads), S::kSmem, s, 1, p, q, k, v);
+  prof_end(s);
+  if (csa_status st = check_launch(what, e); st != CSA_OK) return st;
+  const int64_t rows = max_rows < S::kRows ? max_rows : S::kRows;
+  // rows of a second tile start at 128 whatever the first tile's unused rows are
+  const int used = rows <= kTile ? static_cast<int>(rows) : S::kRows;
+  e = launch_pdl(gqa_merge_kernel<DV, S::kRows>, dim3(grid, (used + 7) / 8), dim3(256), 0, s, 1, p);
+  return check_launch(what, e);
+}
+
+template <bool PAGED>
+csa_status dispatch(const char* what, Params& p, const gqa::Heads& h, const CUtensorMap& q, const CUtensorMap& k,
+                    const CUtensorMap& v, int64_t max_rows, cudaStream_t s) {
+  const bool single = max_rows <= kTile;
+  p.g.tpb = p.g.tpt * (single ? 1 : 2);
+#define CSA_GQA_CASE(A, B)                                                                       \
+  if (h.dqk == A && h.dv == B)                                                                   \
+    return single ? launch<A, B, PAGED, true>(what, p, q, k, v, max_rows, s)                     \
+                  : launch<A, B, PAGED, false>(what, p, q, k, v, max_rows, s);
+  CSA_GQA_CASE(192, 128)
+  CSA_GQA_CASE(128, 128)
+  CSA_GQA_CASE(64, 64)
+#undef CSA_GQA_CASE
+  return fail(CSA_ERR_UNSUPPORTED, "%s: channel widths %d/%d", what, h.dqk, h.dv);
+}
+
+// No item of any sequence has more rows than this.
+int64_t rows_bound(int64_t max_q, int64_t G) { return max_q > 2 * kTile ? 2 * kTile : (max_q * G > 2 * kTile ? 2 * kTile : max_q * G); }
+
+csa_status check_workspace(const char* what, int64_t max_q, const gqa::Heads& h, const void* workspace, size_t bytes) {
+  const size_t need = layout(rows_bound(max_q, h.G), h.dv).bytes;
+  if (workspace == nullptr || bytes < need)
+    return fail(CSA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", what, need,
+                workspace == nullptr ? static_cast<size_t>(0) : bytes);
+  CSA_REQUIRE(aligned16(workspace), "%s: workspace is not 16-byte aligned", what);
+  return CSA_OK;
+}
+
+csa_status run(const char* what, bool paged, Params& p, const gqa::Heads& h, const CUtensorMap& q, const CUtensorMap& k,
+               const CUtensorMap& v, int64_t max_q, float scale, void* out, float* lse, void* workspace,
+               cudaStream_t s) {
+  const int64_t max_rows = rows_bound(max_q, h.G);
+  const Workspace w = layout(max_rows, h.dv);
+  p.Hq = h.Hkv * h.G;
+  p.scale = scale;
+  p.scale_log2 = scale * kLog2e;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  p.ml = reinterpret_cast<float2*>(ws + w.ml);
+  p.meta = reinterpret_cast<int4*>(ws + w.meta);
+  return paged ? dispatch<true>(what, p, h, q, k, v, max_rows, s) : dispatch<false>(what, p, h, q, k, v, max_rows, s);
+}
+
+}  // namespace
+}  // namespace csa
+
+extern "C" {
+
+size_t gqa_dense_workspace_size(int64_t max_q, int32_t H, int32_t H_kv, int32_t d_v) {
+  if (max_q <= 0 || H_kv <= 0 || H < H_kv || d_v <= 0) return 0;
+  return csa::layout(csa::rows_bound(max_q, H / H_kv), d_v).bytes;
+}
+
+csa_status gqa_dense_packed(const void* q, const void* k, const void* v, const csa_packed* packed, int32_t H,
+                            int32_t H_kv, int32_t d_qk, int32_t d_v, float scale, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace csa;
+  const char* what = "gqa_dense_packed";
+  clear_error();
+  CSA_REQUIRE(packed != nullptr, "%s: packed is NULL", what);
+  gqa::Heads h;
+  if (csa_status st = gqa::check_heads(what, H, H_kv, d_qk, d_v, &h); st != CSA_OK) return st;
+  if (csa_status st = gqa::check_scale(what, scale); st != CSA_OK) return st;
+  CSA_REQUIRE(packed->n_seqs >= 0 && packed->max_tokens >= 0, "%s: negative sizes", what);
+  CSA_REQUIRE(packed->total_tokens >= 0 && packed->total_tokens < (int64_t(1) << 31),
+              "%s: total_tokens must be in [0, 2^31)", what);
+  CSA_REQUIRE(packed->max_tokens <= packed->total_tokens, "%s: max_tokens is larger than total_tokens", what);
+  if (packed->n_seqs == 0 || packed->total_tokens == 0) return CSA_OK;
+  CSA_REQUIRE(packed->max_tokens >= 1, "%s: max_tokens is 0 but there are tokens", what);
+  CSA_REQUIRE_PTR(q);
+  CSA_REQUIRE_PTR(k);
+  CSA_REQUIRE_PTR(v);
+  CSA_REQUIRE_PTR(out);
+  CSA_REQUIRE_PTR(packed->cu_tokens);
+  CSA_REQUIRE(lse == nullptr || aligned16(lse), "%s: lse is not 16-byte aligned", what);
+  if (csa_status st = check_workspace(what, packed->max_tokens, h, workspace, workspace_bytes); st != CSA_OK) return st;
+  Params p;
+  memset(&p, 0, sizeof(p));
+  p.g.cu_q = packed->cu_tokens;
+  p.g.cache_len = nullptr;
+  p.g.n_seqs = packed->n_seqs;
+  p.g.max_len = 0x7fffffff;
+  p.g.total_q = packed->total_tokens;
+  p.g.Hkv = h.Hkv;
+  p.g.G = h.G;
+  p.g.tpt = kTile / h.G;
+  p.page = kTile;
+  CUtensorMap qm, km, vm;
+  const uint64_t rows = static_cast<uint64_t>(packed->total_tokens);
+  csa_status st = gqa::map_tokens(what, &qm, q, h.dqk, H, rows, h.G, p.g.tpt);
+  if (st == CSA_OK) st = gqa::map_tokens(what, &km, k, h.dqk, H_kv, rows, 1, kTile);
+  if (st == CSA_OK) st = gqa::map_tokens(what, &vm, v, h.dv, H_kv, rows, 1, kTile);
+  if (st != CSA_OK) return st;
+  return run(what, false, p, h, qm, km, vm, packed->max_tokens, scale, out, lse, workspace,
+             static_cast<cudaStream_t>(stream));
+}
+
+csa_status gqa_dense_paged(const void* q, const gqa_cache* cache, const gqa_batch* batch, int32_t H, float scale,
+                           void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace csa;
+  const char* what = "gqa_dense_paged";
+  clear_error();
+  gqa::Heads h;
+  if (csa_status st = gqa::check_paged(what, cache, batch, H, &h); st != CSA_OK) return st;
+  if (csa_status st = gqa::check_scale(what, scale); st != CSA_OK) return st;
+  if (batch->n_seqs == 0 || batch->total_q == 0) return CSA_OK;
+  if (csa_status st = gqa::check_pool(what, cache, batch, true); st != CSA_OK) return st;
+  CSA_REQUIRE_PTR(q);
+  CSA_REQUIRE_PTR(out);
+  CSA_REQUIRE(lse == nullptr || aligned16(lse), "%s: lse is not 16-byte aligned", what);
+  if (csa_status st = check_workspace(what, batch->max_q, h, workspace, workspace_bytes); st != CSA_OK) return st;
+  Params p;
+  memset(&p, 0, sizeof(p));
+  p.g.cu_q = batch->cu_q;
+  p.g.cache_len = batch->cache_len;
+  p.g.n_seqs = batch->n_seqs;
+  p.g.max_len = gqa::max_len(cache, batch);
+  p.g.total_q = batch->total_q;
+  p.g.Hkv = h.Hkv;
+  p.g.G = h.G;
+  p.g.tpt = kTile / h.G;
+  p.block_table = batch->block_table;
+  p.max_pages = batch->max_pages;
+  p.page = cache->page_size;
+  p.n_pages = static_cast<int>(cache->n_pages);
+  p.kv_rows = cache->n_pages * h.Hkv * cache->page_size;
+  CUtensorMap qm, km, vm;
+  csa_status st = gqa::map_tokens(what, &qm, q, h.dqk, H, static_cast<uint64_t>(batch->total_q), h.G, p.g.tpt);
+  if (st == CSA_OK) st = gqa::map_rows(what, &km, cache->k, h.dqk, static_cast<uint64_t>(p.kv_rows), cache->page_size);
+  if (st == CSA_OK) st = gqa::map_rows(what, &vm, cache->v, h.dv, static_cast<uint64_t>(p.kv_rows), cache->page_size);
+  if (st != CSA_OK) return st;
+  return run(what, true, p, h, qm, km, vm, batch->max_q, scale, out, lse, workspace,
+             static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
+
+namespace csa {
+// Reads (and optionally clears) this unit's device error word.
+CSA_DEFINE_DEVICE_ERROR_READER(gqa_device_error)
+}  // namespace csa
