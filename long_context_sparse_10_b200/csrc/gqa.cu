@@ -71,7 +71,7 @@ struct Shape {
   static constexpr size_t kKOff = static_cast<size_t>(kQTiles) * kQBytes;
   static constexpr size_t kVOff = kKOff + static_cast<size_t>(kKStages) * kQBytes;
   static constexpr size_t kMiscOff = kVOff + static_cast<size_t>(kVStages) * kVBytes;
-  static constexpr size_t kBars = 2 * kKStages + 2 * kVStages + 12;
+  static constexpr size_t kBars = 2 * kKStages + 2 * kVStages + 14;
   // barriers | partition scratch (40 int64) | TMEM slot | (reference, sum) of stream 1
   static constexpr size_t kStatOff = kMiscOff + 8 * kBars + 8 * 40 + 16;
   static constexpr size_t kSmem = ((kStatOff + 15) / 16) * 16 + kWgThreads * 8 + 1024;
@@ -177,6 +177,11 @@ __device__ __forceinline__ void regs_down() {
 // n0, n1 (two tiles of rows), or one tile of rows: even and odd key tiles.
 __device__ __forceinline__ bool active(bool one, int s, int j, int n0) { return one ? (j & 1) == s : (s == 1 || j < n0); }
 
+// Whether stream s clears the rows of V past the sequence's end in tile j: the first stream to use the tile.
+__device__ __forceinline__ bool clears_tail(bool one, int s, int j, int n0, int L) {
+  return L - j * kTile < kTile && (one || s == 0 || j >= n0);
+}
+
 template <int DQK, int DV, bool PAGED, bool SINGLE>
 __global__ void __launch_bounds__(kThreads, 1)
     gqa_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
@@ -198,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pfull = sfull + 2;             // [2] probabilities of a stream are in TMEM
   uint64_t* odone = pfull + 2;             // [2] a stream's PV product is complete
   uint64_t* oempty = odone + 2;            // [2] a stream's O has been read out
-  int64_t* scratch = reinterpret_cast<int64_t*>(oempty + 2);
+  uint64_t* vland = oempty + 2;            // [2] V of a stream's tile with keys past the end has arrived
+  int64_t* scratch = reinterpret_cast<int64_t*>(vland + 2);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(scratch + 40);
   float2* stat = reinterpret_cast<float2*>(smem + ((S::kStatOff + 15) / 16) * 16);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -220,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::bar_init(&pfull[i], 4);
       tc::bar_init(&odone[i], 1);
       tc::bar_init(&oempty[i], kWgThreads);
+      tc::bar_init(&vland[i], 1);
     }
     tc::bar_init_fence();
   }
@@ -355,7 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t b = v_desc + sv * (S::kVBytes >> 4);
           for (int s = 0; s < 2 && healthy; ++s) {
             if (!active(one, s, j, n0)) continue;
-            healthy = tc::bar_wait(&vfull[sv], (t / S::kVStages) & 1) && tc::bar_wait(&pfull[s], np[s] & 1);
+            healthy = tc::bar_wait(&vfull[sv], (t / S::kVStages) & 1);
+            if (clears_tail(one, s, j, n0, w.q.L)) bar_arrive(&vland[s]);
+            healthy = healthy && tc::bar_wait(&pfull[s], np[s] & 1);
             if (first[s] && items > 0) healthy = healthy && tc::bar_wait(&oempty[s], (items - 1) & 1);
             if (!healthy) break;
             tc::fence_after_sync();
@@ -394,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk w;
     bool healthy = true;
     int items = 0, base = 0;
-    int ns = 0;  // this stream's tiles so far
+    int ns = 0;     // this stream's tiles so far
+    int tails = 0;  // and those whose V it cleared behind the sequence's end
     int first_blk = 0, first_s = 0, first_h = 0, flags = 0;
     for (bool more = w.begin(g, share); more; more = w.next(g), ++items) {
       const bool one = w.one;
@@ -479,10 +489,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_wait_st();
         }
         // keys past the sequence's end share its last tile: their values may be anything (another sequence,
-        // a page never written), and 0 x NaN is NaN, so those rows of V become zeros
-        if (w.q.L - k0 < kTile) {
+        // a page never written), and 0 x NaN is NaN, so those rows of V become zeros.  The MMA thread, which
+        // waits for every V tile in turn, says when this one is there.
+        if (clears_tail(one, s, j, n0, w.q.L)) {
           const int t = base + j - w.t0, sv = t % S::kVStages;
-          if (healthy) healthy = tc::bar_wait(&vfull[sv], (t / S::kVStages) & 1);
+          if (healthy) healthy = tc::bar_wait(&vland[s], tails & 1);
+          ++tails;
           const int from = w.q.L - k0 > 0 ? w.q.L - k0 : 0;
           uint8_t* vb = Vs + sv * S::kVBytes;
           for (int i = r; i < (kTile - from) * 8 * S::kVc; i += kWgThreads) {

@@ -83,6 +83,27 @@ def test_packed_prompts(lens, Hkv, G, dims):
         a += s
 
 
+@pytest.mark.parametrize("dims", DIMS)
+def test_a_prompt_batch_gives_the_same_bits_every_time(dims):
+    # last blocks of a few tokens (one tile of rows, two streams over its keys) beside full ones, on every SM
+    lens = [2048, 513, 1, 777, 0, 4000, 1025, 128, 31, 1500, 2049]
+    g = np.random.default_rng(6)
+    n, Hkv, G = sum(lens), 4, 4
+    q, k, v = bf16(g, n, Hkv * G, dims[0]), bf16(g, n, Hkv, dims[0]), bf16(g, n, Hkv, dims[1])
+    args = (q.to(DEV), k.to(DEV), v.to(DEV), csa.Packed(lens, 1), 1 / math.sqrt(dims[0]))
+    runs = [csa.gqa_dense_packed(*args) for _ in range(30)]
+    torch.cuda.synchronize()
+    no_device_error()
+    for out, lse in runs[1:]:
+        assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
+    a = 0
+    for s in lens:  # the last rows of each sequence
+        b = max(s - 3, 0)
+        ref, _, size = R.attend(f64(q[a + b:a + s]), f64(k[a:a + s]), f64(v[a:a + s]), args[4], b)
+        check_out(f64(runs[0][0][a + b:a + s]), ref, size, f"sequence at {a}")
+        a += s
+
+
 class Case:
     """A paged cache with its pages in random order; what no token lies in holds NaN."""
 
