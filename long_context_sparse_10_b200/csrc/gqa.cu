@@ -13,7 +13,7 @@
 //                   scores read from TMEM, one pass with a running reference
 //                   and sum, probabilities written back to TMEM as bf16
 //   warp 8          TMA producer (128-byte swizzled K and V tiles, rings)
-//   warp 9          one thread issues the MMAs: S = Q K^T (both operands in
+//   warp 9          issues the MMAs: S = Q K^T (both operands in
 //                   shared memory), O += P V (P from TMEM, V as it lies in
 //                   memory, channel-major for the MMA)
 //   warps 10, 11    none (they complete the warpgroup whose registers move)
@@ -169,6 +169,13 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
+// One lane of a converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
 }
@@ -245,21 +252,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool healthy = true;
     int items = 0, tk = 0, tv = 0;
     for (bool more = w.begin(g, share); more && healthy; more = w.next(g), ++items) {
-      // queries: one or two tiles
-      if (items > 0) {
-        healthy = tc::bar_wait(&qempty[0], (items - 1) & 1) && tc::bar_wait(&qempty[1], (items - 1) & 1);
-        if (!healthy) break;
-      }
-      if (lane == 0) {
-        const int nt = w.one ? 1 : 2;
-        for (int s = 0; s < nt; ++s) {
-          bar_expect(&qfull[s], rows_q * 128u * S::kQc);
-          const int tok = w.q.row0 + w.blk * g.tpb + s * g.tpt;
-          for (int c = 0; c < S::kQc; ++c)
-            tc::tma_load_3d(Qs + s * S::kQBytes + c * (kTile * 128), &qmap, c * 64, w.h * g.G, tok, &qfull[s]);
-        }
-      }
-      __syncwarp();
       // a tile's 128 rows: one box (prompts), or one box per page and 64-channel block
       const int live = PAGED ? (w.q.L + p.page - 1) / p.page : 0;
       const int ppt = PAGED ? kTile / p.page : 1;
@@ -294,9 +286,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (is_v) ++tv; else ++tk;
         return true;
       };
-      // K runs one tile ahead of V, as the products use them
+      // K runs one tile ahead of V, as the products use them; an item's first K tile does not wait for the
+      // item before to be done with its queries
       int row_cur = PAGED && lane < ppt ? page_row(w.t0, lane) : 0;
       healthy = load_tile(false, w.t0, row_cur);
+      if (!healthy) break;
+      // queries: one or two tiles
+      if (items > 0) {
+        healthy = tc::bar_wait(&qempty[0], (items - 1) & 1) && tc::bar_wait(&qempty[1], (items - 1) & 1);
+        if (!healthy) break;
+      }
+      if (lane == 0) {
+        const int nt = w.one ? 1 : 2;
+        for (int s = 0; s < nt; ++s) {
+          bar_expect(&qfull[s], rows_q * 128u * S::kQc);
+          const int tok = w.q.row0 + w.blk * g.tpb + s * g.tpt;
+          for (int c = 0; c < S::kQc; ++c)
+            tc::tma_load_3d(Qs + s * S::kQBytes + c * (kTile * 128), &qmap, c * 64, w.h * g.G, tok, &qfull[s]);
+        }
+      }
+      __syncwarp();
       for (int j = w.t0; j < w.t1 && healthy; ++j) {
         int row_next = row_cur;
         if (j + 1 < w.t1) {
@@ -309,83 +318,112 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     regs_down();
-    // ===================== MMA issue (one thread) =====================
-    if (lane == 0) {
-      constexpr uint32_t id_qk = tc::idesc_bf16(kTile, kTile, false, false);
-      constexpr uint32_t id_pv = tc::idesc_bf16(kTile, DV, true, false);
-      const uint64_t q_desc = tc::desc_sw128(smem_u32(Qs), 16, 1024), k_desc = tc::desc_sw128(smem_u32(Ks), 16, 1024);
-      const uint64_t v_desc = tc::desc_sw128(smem_u32(Vs), kTile * 128, 1024);
-      Walk w;
-      bool healthy = true;
-      int items = 0, pairs = 0;
-      int base = 0;                 // this CTA's tiles before the item
-      int np[2] = {0, 0};           // PV products issued per stream
-      for (bool more = w.begin(g, share); more && healthy; more = w.next(g), ++items) {
-        const bool one = w.one;
-        const int n0 = one ? w.n : (w.blk * g.tpb + g.tpt + (w.q.L - w.q.nq) + kTile - 1) / kTile;
-        healthy = tc::bar_wait(&qfull[0], items & 1);
-        if (!one) {
-          healthy = healthy && tc::bar_wait(&qfull[1], pairs & 1);
-          ++pairs;
-        }
-        tc::fence_after_sync();
-        if (!healthy) break;
-        auto qk = [&](int s, int j) {
-          const int t = base + j - w.t0, st = t % S::kKStages;
-          if (!tc::bar_wait(&kfull[st], (t / S::kKStages) & 1)) return false;
-          tc::fence_after_sync();
-          const uint64_t a = q_desc + (one ? 0 : s * (S::kQBytes >> 4)), b = k_desc + st * (S::kQBytes >> 4);
+    // ===================== MMA issue (the whole warp walks, one lane issues) =====================
+    // The operands of an MMA are uniform registers: the warp stays converged and descriptors advance by
+    // constants, so that issuing eight of them takes less time than the tensor core needs for one.
+    constexpr uint32_t id_qk = tc::idesc_bf16(kTile, kTile, false, false);
+    constexpr uint32_t id_pv = tc::idesc_bf16(kTile, DV, true, false);
+    const uint64_t q_desc = tc::desc_sw128(smem_u32(Qs), 16, 1024), k_desc = tc::desc_sw128(smem_u32(Ks), 16, 1024);
+    const uint64_t v_desc = tc::desc_sw128(smem_u32(Vs), kTile * 128, 1024);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    Walk w;
+    bool healthy = true;
+    int items = 0, pairs = 0;
+    int base = 0;              // this CTA's tiles before the item
+    int np0 = 0, np1 = 0;      // PV products issued per stream
+    for (bool more = w.begin(g, share); more && healthy; more = w.next(g), ++items) {
+      const bool one = w.one;
+      const int n0 = one ? w.n : (w.blk * g.tpb + g.tpt + (w.q.L - w.q.nq) + kTile - 1) / kTile;
+      const int t0 = w.t0, t1 = w.t1, L = w.q.L;
+      healthy = tc::bar_wait(&qfull[0], items & 1);
+      if (!one) {
+        healthy = healthy && tc::bar_wait(&qfull[1], pairs & 1);
+        ++pairs;
+      }
+      tc::fence_after_sync();
+      if (!healthy) break;
+      auto qk = [&](int s, int j) {
+        const int t = base + j - t0, st = t % S::kKStages;
+        const uint64_t a = q_desc + (one ? 0 : s * (S::kQBytes >> 4));
+        const uint64_t b = k_desc + __shfl_sync(0xffffffffu, st, 0) * (S::kQBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < DQK / 16; ++k) {
             const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;  // descriptors count 16-byte units
-            tc::mma_bf16_ss(tmem + s * kTile, a + o, b + o, id_qk, k != 0 ? 1u : 0u);
+            tc::mma_bf16_ss(tm + s * kTile, a + o, b + o, id_qk, k != 0 ? 1u : 0u);
           }
           tc::mma_commit(&sfull[s]);
           if (one || s == 1) {  // the tile's last use as K
             tc::mma_commit(&kempty[st]);
-            if (j == w.t1 - 1) {
+            if (j == t1 - 1) {
               tc::mma_commit(&qempty[0]);
               tc::mma_commit(&qempty[1]);
             }
           }
-          return true;
-        };
-        bool first[2] = {true, true};
-        // the first scores of each stream
-        for (int s = 0; s < 2 && healthy; ++s) {
-          const int j = one ? w.t0 + s : w.t0;
-          const int st = one ? (j & 1) : s;
-          if (j < w.t1 && active(one, st, j, n0)) healthy = qk(st, j);
         }
-        for (int j = w.t0; j < w.t1 && healthy; ++j) {
-          const int t = base + j - w.t0, sv = t % S::kVStages;
-          const uint64_t b = v_desc + sv * (S::kVBytes >> 4);
-          for (int s = 0; s < 2 && healthy; ++s) {
-            if (!active(one, s, j, n0)) continue;
-            healthy = tc::bar_wait(&vfull[sv], (t / S::kVStages) & 1);
-            if (clears_tail(one, s, j, n0, w.q.L)) bar_arrive(&vland[s]);
-            healthy = healthy && tc::bar_wait(&pfull[s], np[s] & 1);
-            if (first[s] && items > 0) healthy = healthy && tc::bar_wait(&oempty[s], (items - 1) & 1);
-            if (!healthy) break;
-            tc::fence_after_sync();
+        __syncwarp();
+      };
+      // K of tile j has arrived (awaited once, by the first stream to use it)
+      auto wait_k = [&](int s, int j) {
+        if (!one && s == 1 && j < n0) return true;
+        const int t = base + j - t0;
+        return tc::bar_wait(&kfull[t % S::kKStages], (t / S::kKStages) & 1);
+      };
+      bool first0 = true, first1 = true;
+      // P V of stream s and tile j, then the stream's next scores
+      auto pv = [&](int s, int j, bool& first, int& np) {
+        const int t = base + j - t0, sv = t % S::kVStages;
+        const int jn = one ? j + 2 : j + 1;
+        const bool more_k = jn < t1 && active(one, s, jn, n0);
+        // what arrives early is awaited before the probabilities, so that nothing stands between the two products
+        bool ok = one || s == 0 || j >= n0 ? tc::bar_wait(&vfull[sv], (t / S::kVStages) & 1) : true;
+        if (more_k) ok = ok && wait_k(s, jn);
+        if (clears_tail(one, s, j, n0, L) && lane == 0) bar_arrive(&vland[s]);
+        if (first && items > 0) ok = ok && tc::bar_wait(&oempty[s], (items - 1) & 1);
+        ok = ok && tc::bar_wait(&pfull[s], np & 1);
+        if (!ok) return false;
+        tc::fence_after_sync();
+        const uint64_t b = v_desc + __shfl_sync(0xffffffffu, sv, 0) * (S::kVBytes >> 4);
+        const uint32_t fresh = first ? 0u : 1u;
+        if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_bf16_ts(tmem + 2 * kTile + s * DV, tmem + s * kTile + k * 8, b + k * (2048 >> 4), id_pv,
-                          (first[s] && k == 0) ? 0u : 1u);
-            tc::mma_commit(&odone[s]);
-            first[s] = false;
-            ++np[s];
-            if (one || s == 1) tc::mma_commit(&vempty[sv]);
-            const int jn = one ? j + 2 : j + 1;
-            if (jn < w.t1 && active(one, s, jn, n0)) healthy = qk(s, jn);
-          }
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_bf16_ts(tm + 2 * kTile + s * DV, tm + s * kTile + k * 8, b + k * (2048 >> 4), id_pv,
+                        k == 0 ? fresh : 1u);
+          tc::mma_commit(&odone[s]);
+          if (one || s == 1) tc::mma_commit(&vempty[sv]);
         }
-        // a stream without a tile here: its previous item's read-out is awaited all the same, so that no
-        // phase of oempty is left two behind
-        for (int s = 0; s < 2; ++s)
-          if (first[s] && items > 0 && healthy) healthy = tc::bar_wait(&oempty[s], (items - 1) & 1);
-        base += w.t1 - w.t0;
+        __syncwarp();
+        first = false;
+        ++np;
+        if (more_k) qk(s, jn);
+        return true;
+      };
+      // the first scores of each stream
+      auto start = [&](int s, int j) {
+        if (j >= t1 || !active(one, s, j, n0) || !wait_k(s, j)) return;
+        tc::fence_after_sync();
+        qk(s, j);
+      };
+      const int odd = one ? (t0 & 1) : 0;
+      if (odd) {
+        start(1, t0);
+        start(0, t0 + 1);
+      } else {
+        start(0, t0);
+        start(1, one ? t0 + 1 : t0);
       }
+      for (int j = t0; j < t1 && healthy; ++j) {
+        if (active(one, 0, j, n0)) healthy = pv(0, j, first0, np0);
+        if (healthy && active(one, 1, j, n0)) healthy = pv(1, j, first1, np1);
+      }
+      // a stream without a tile here: its previous item's read-out is awaited all the same, so that no
+      // phase of oempty is left two behind
+      if (items > 0 && healthy) {
+        if (first0) healthy = tc::bar_wait(&oempty[0], (items - 1) & 1);
+        if (first1) healthy = healthy && tc::bar_wait(&oempty[1], (items - 1) & 1);
+      }
+      base += t1 - t0;
     }
   } else if (warp >= 10) {
     regs_down();
