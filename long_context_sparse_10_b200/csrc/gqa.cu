@@ -22,8 +22,11 @@
 // both read the same K/V tile; an item of at most one tile (decode) gives its
 // even key tiles to one stream and its odd ones to the other, with their own
 // references, sums and accumulators, joined in the epilogue.
-// TMEM: S of stream 0 and 1 (128 fp32 columns each; P overlays S), O of
-// stream 0 and 1.
+// TMEM: S of stream 0 and 1 (128 fp32 columns each; the probabilities overlay
+// their scores), O of stream 0 and 1.  A stream's chain is scores -> maximum ->
+// exponentials -> product -> next scores; the probabilities are handed over in
+// two halves of 64 keys, so that the first half's product runs under the second
+// half's exponentials.
 //
 // The softmax reference of a row follows its running maximum lazily: O and the
 // sum are rescaled only when a tile's maximum exceeds the reference by more
@@ -52,10 +55,12 @@ using gqa::Seq;
 using gqa::Walk;
 
 constexpr int kThreads = 384;
-// Registers: 384 threads start with 168 each; the softmax warpgroups take 208 (a row of scores is 128 of them)
+// Registers: 384 threads start with 168 each; the softmax warpgroups take more (a row of scores is 128 of them)
 // and the third warpgroup gives up what it does not need: 2 * 208 + 88 = 3 * 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kWgThreads = 128;
+constexpr int kStep = 64;  // keys of half a tile
+constexpr int kFmas = 2;   // of 8 pairs of exponentials, those on the fp32 units
 constexpr float kRescaleLog2 = 8.f;
 
 // SINGLE: every item of the call fits one 128-row tile (decode), so one Q tile
@@ -71,7 +76,7 @@ struct Shape {
   static constexpr size_t kKOff = static_cast<size_t>(kQTiles) * kQBytes;
   static constexpr size_t kVOff = kKOff + static_cast<size_t>(kKStages) * kQBytes;
   static constexpr size_t kMiscOff = kVOff + static_cast<size_t>(kVStages) * kVBytes;
-  static constexpr size_t kBars = 2 * kKStages + 2 * kVStages + 14;
+  static constexpr size_t kBars = 2 * kKStages + 2 * kVStages + 16;
   // barriers | partition scratch (40 int64) | TMEM slot | (reference, sum) of stream 1
   static constexpr size_t kStatOff = kMiscOff + 8 * kBars + 8 * 40 + 16;
   static constexpr size_t kSmem = ((kStatOff + 15) / 16) * 16 + kWgThreads * 8 + 1024;
@@ -84,7 +89,8 @@ struct Params {
   int max_pages, page, n_pages;
   int64_t kv_rows;             // rows of the page pool: n_pages * Hkv * page
   int Hq;
-  float scale, scale_log2;
+  bool wide;                   // out and the workspace start on 32-byte boundaries
+  float scale_log2;
   __nv_bfloat16* out;
   float* lse;
   float* part;  // [2 C, rows, DV] unnormalised partial outputs
@@ -164,9 +170,120 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
 __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
+// Wait of a converged warp for a barrier's phase.  Almost always the phase is there or arrives within one try: that
+// path has one try and a vote, so that no branch of it diverges (a loop whose exit is each lane's own costs 150
+// clocks more).  The bounded loop is for the rest; false, for all lanes, when it runs out.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit = tc::kWaitLimit) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  bool all = __all_sync(0xffffffffu, ok != 0);
+  if (!all) all = __all_sync(0xffffffffu, tc::bar_wait_bounded(bar, parity, limit));
+  return all;
+}
+// Arrives where `on` holds, without a branch.
+__device__ __forceinline__ void bar_arrive_if(uint64_t* bar, bool on, uint32_t n = 1) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 _, [%0], %2;\n}\n" ::"r"(
+                   smem_u32(bar)),
+               "r"(static_cast<uint32_t>(on)), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 32 bytes in one store where the address allows it: a warp whose lanes write 32 different rows pays per row.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
 __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) { tc::bar_arrive_expect_tx(bar, bytes); }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+// (a0, a1) + (b, b) and (a0, a1) * (b0, b1) + (c, c), as above.
+__device__ __forceinline__ void add2s(float& d0, float& d1, float a0, float a1, float b) {
+  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %4};\nadd.rn.f32x2 d, a, b;\n"
+      "mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b));
+}
+__device__ __forceinline__ void sub2(float& d0, float& d1, float a0, float a1) {  // d - a
+  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %4};\nmov.b64 d, {%0, %1};\n"
+      "fma.rn.f32x2 d, a, b, d;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1), "f"(-1.f));
+}
+__device__ __forceinline__ void mul_add2(float& d0, float& d1, float b0, float b1, float c) {  // d * b + c
+  asm("{\n.reg .b64 b, c, d;\nmov.b64 b, {%2, %3};\nmov.b64 c, {%4, %4};\nmov.b64 d, {%0, %1};\n"
+      "fma.rn.f32x2 d, d, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "+f"(d0), "+f"(d1)
+      : "f"(b0), "f"(b1), "f"(c));
+}
+
+// 2^x of two numbers on the fp32 units.  x = n + f with n the nearest whole
+// number (adding 1.5 * 2^23 leaves it in the low bits of the sum) and |f| <= 1/2;
+// 2^f by its minimax polynomial of degree 4 in relative error (fitted by
+// iteratively reweighted least squares; 2.7e-6 off at most in fp32), and n is
+// added to the exponent.  Below 2^-126 the result stays there.
+__device__ __forceinline__ void exp2_fma2(float& x0, float& x1) {
+  constexpr float kMagic = 12582912.f;
+  x0 = fmaxf(x0, -126.f);
+  x1 = fmaxf(x1, -126.f);
+  float t0, t1, n0, n1;
+  add2s(t0, t1, x0, x1, kMagic);
+  add2s(n0, n1, t0, t1, -kMagic);
+  sub2(x0, x1, n0, n1);
+  float y0, y1;
+  fma2(y0, y1, x0, x1, 0.009570102207362652f, 0.05591785907745361f);
+  mul_add2(y0, y1, x0, x1, 0.240247443318367f);
+  mul_add2(y0, y1, x0, x1, 0.6931217908859253f);
+  mul_add2(y0, y1, x0, x1, 0.9999992847442627f);
+  x0 = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23));
+  x1 = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23));
+}
+
+// Probabilities 2^(v * a + b) of a row's 64 scores: written as bf16 pairs to
+// 32 TMEM columns; returns their sum (of the unrounded values).  The
+// exponential unit gives a warp one result in 8 clocks, 2048 for two rows of 128
+// keys, as long as their MMAs; so FMAS of every 8 pairs are computed
+// on the fp32 units instead, which takes those about as long.
+template <int FMAS>
+__device__ __forceinline__ float probabilities(float* v, float a, float b, uint32_t tP) {
+  float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+  for (int c = 0; c < kStep / 32; ++c) {
+    float pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float* e = v + 32 * c + 2 * i;
+      fma2(e[0], e[1], e[0], e[1], a, b);
+      if (i % 8 >= 8 - FMAS) {
+        exp2_fma2(e[0], e[1]);
+      } else {
+        e[0] = exp2_approx(e[0]);
+        e[1] = exp2_approx(e[1]);
+      }
+      if (i & 1)
+        add2(l2, l3, e[0], e[1]);
+      else
+        add2(l0, l1, e[0], e[1]);
+      pk[i] = __uint_as_float(pack_bf16x2(e[0], e[1]));
+    }
+    tmem_st16(tP + 16 * c, pk);
+  }
+  return (l0 + l1) + (l2 + l3);
 }
 
 // One lane of a converged warp (always the same one).
@@ -180,13 +297,34 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
 }
 
-// Whether stream s works on key tile j of an item whose tiles per stream are
-// n0, n1 (two tiles of rows), or one tile of rows: even and odd key tiles.
-__device__ __forceinline__ bool active(bool one, int s, int j, int n0) { return one ? (j & 1) == s : (s == 1 || j < n0); }
+// 64 scores of a row, -inf from column `vis` on where the tile is masked.
+__device__ __forceinline__ void load_scores(float* v, uint32_t taddr, bool masked, int vis) {
+  tmem_ld32_async(taddr, v);
+  tmem_ld32_async(taddr + 32, v + 32);
+  tc::tmem_wait_ld();
+  fence_regs(v);
+  fence_regs(v + 32);
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) v[i] = i < vis ? v[i] : -INFINITY;
+  }
+}
 
+// Halves (64 keys) of key tile j that stream s works on.  ks: the keys its last row sees.  An item of one tile of rows
+// gives its even and odd key tiles to the two streams.
+__device__ __forceinline__ int steps_of(bool one, int s, int j, int ks) {
+  const int left = ks - j * kTile;
+  if ((one && (j & 1) != s) || left <= 0) return 0;
+  return left > kStep ? 2 : 1;
+}
+// Keys the last row of stream s sees.
+__device__ __forceinline__ int stream_keys(const Geometry& g, const Walk& w, int s) {
+  const int tok = w.blk * g.tpb + (w.one ? 1 : s + 1) * g.tpt;
+  return w.q.L - w.q.nq + (tok < w.q.nq ? tok : w.q.nq);
+}
 // Whether stream s clears the rows of V past the sequence's end in tile j: the first stream to use the tile.
-__device__ __forceinline__ bool clears_tail(bool one, int s, int j, int n0, int L) {
-  return L - j * kTile < kTile && (one || s == 0 || j >= n0);
+__device__ __forceinline__ bool clears_tail(bool one, int s, int j, int ks0, int L) {
+  return L - j * kTile < kTile && (one || s == 0 || ks0 <= j * kTile);
 }
 
 template <int DQK, int DV, bool PAGED, bool SINGLE>
@@ -207,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* qfull = vempty + S::kVStages;  // [2]
   uint64_t* qempty = qfull + 2;            // [2]
   uint64_t* sfull = qempty + 2;            // [2] scores of a stream are in TMEM
-  uint64_t* pfull = sfull + 2;             // [2] probabilities of a stream are in TMEM
-  uint64_t* odone = pfull + 2;             // [2] a stream's PV product is complete
+  uint64_t* pfull = sfull + 2;             // [stream][half] probabilities are in TMEM
+  uint64_t* odone = pfull + 4;             // [2] a stream's product of a tile is complete
   uint64_t* oempty = odone + 2;            // [2] a stream's O has been read out
   uint64_t* vland = oempty + 2;            // [2] V of a stream's tile with keys past the end has arrived
   int64_t* scratch = reinterpret_cast<int64_t*>(vland + 2);
@@ -230,7 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::bar_init(&qfull[i], 1);
       tc::bar_init(&qempty[i], 1);
       tc::bar_init(&sfull[i], 1);
-      tc::bar_init(&pfull[i], 4);
+      tc::bar_init(&pfull[2 * i], 4);
+      tc::bar_init(&pfull[2 * i + 1], 4);
       tc::bar_init(&odone[i], 1);
       tc::bar_init(&oempty[i], kWgThreads);
       tc::bar_init(&vland[i], 1);
@@ -239,6 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 9) tc::tmem_alloc(tslot, 512);
   const gqa::Share share = gqa::find_share(g, blockIdx.x, gridDim.x, scratch);
+  Walk w;
+  bool more = w.begin(g, share);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -248,10 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     regs_down();
     // ===================== TMA producer =====================
-    Walk w;
     bool healthy = true;
     int items = 0, tk = 0, tv = 0;
-    for (bool more = w.begin(g, share); more && healthy; more = w.next(g), ++items) {
+    for (; more && healthy; more = w.next(g), ++items) {
       // a tile's 128 rows: one box (prompts), or one box per page and 64-channel block
       const int live = PAGED ? (w.q.L + p.page - 1) / p.page : 0;
       const int ppt = PAGED ? kTile / p.page : 1;
@@ -269,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* full = is_v ? &vfull[st] : &kfull[st];
         uint64_t* empty = is_v ? &vempty[st] : &kempty[st];
         uint8_t* dst = is_v ? Vs + st * S::kVBytes : Ks + st * S::kQBytes;
-        if (use > 0 && !tc::bar_wait(empty, (use - 1) & 1)) return false;
+        if (use > 0 && !wait_warp(empty, (use - 1) & 1)) return false;
         if (lane == 0) bar_expect(full, static_cast<uint32_t>(is_v ? S::kVBytes : S::kQBytes));
         __syncwarp();
         if constexpr (PAGED) {
@@ -293,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!healthy) break;
       // queries: one or two tiles
       if (items > 0) {
-        healthy = tc::bar_wait(&qempty[0], (items - 1) & 1) && tc::bar_wait(&qempty[1], (items - 1) & 1);
+        healthy = wait_warp(&qempty[0], (items - 1) & 1) && wait_warp(&qempty[1], (items - 1) & 1);
         if (!healthy) break;
       }
       if (lane == 0) {
@@ -326,102 +466,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t q_desc = tc::desc_sw128(smem_u32(Qs), 16, 1024), k_desc = tc::desc_sw128(smem_u32(Ks), 16, 1024);
     const uint64_t v_desc = tc::desc_sw128(smem_u32(Vs), kTile * 128, 1024);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    Walk w;
     bool healthy = true;
     int items = 0, pairs = 0;
-    int base = 0;              // this CTA's tiles before the item
-    int np0 = 0, np1 = 0;      // PV products issued per stream
-    for (bool more = w.begin(g, share); more && healthy; more = w.next(g), ++items) {
+    int base = 0;                                       // this CTA's tiles before the item
+    uint32_t parity = 0;                                // of pfull[stream][half], a bit each
+    for (; more && healthy; more = w.next(g), ++items) {
       const bool one = w.one;
-      const int n0 = one ? w.n : (w.blk * g.tpb + g.tpt + (w.q.L - w.q.nq) + kTile - 1) / kTile;
       const int t0 = w.t0, t1 = w.t1, L = w.q.L;
-      healthy = tc::bar_wait(&qfull[0], items & 1);
+      const int ks0 = stream_keys(g, w, 0), ks1 = stream_keys(g, w, 1);
+      healthy = wait_warp(&qfull[0], items & 1);
       if (!one) {
-        healthy = healthy && tc::bar_wait(&qfull[1], pairs & 1);
+        healthy = healthy && wait_warp(&qfull[1], pairs & 1);
         ++pairs;
       }
-      tc::fence_after_sync();
-      if (!healthy) break;
+      // S = Q K^T of a tile
       auto qk = [&](int s, int j) {
-        const int t = base + j - t0, st = t % S::kKStages;
-        const uint64_t a = q_desc + (one ? 0 : s * (S::kQBytes >> 4));
-        const uint64_t b = k_desc + __shfl_sync(0xffffffffu, st, 0) * (S::kQBytes >> 4);
+        const int st = (base + j - t0) % S::kKStages;
+        const uint64_t a = q_desc + __shfl_sync(0xffffffffu, one ? 0 : s * (S::kQBytes >> 4), 0);
+        const uint64_t b = k_desc + __shfl_sync(0xffffffffu, st * (S::kQBytes >> 4), 0);
+        const uint32_t d = __shfl_sync(0xffffffffu, tm + s * kTile, 0);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < DQK / 16; ++k) {
             const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;  // descriptors count 16-byte units
-            tc::mma_bf16_ss(tm + s * kTile, a + o, b + o, id_qk, k != 0 ? 1u : 0u);
+            tc::mma_bf16_ss(d, a + o, b + o, id_qk, k != 0 ? 1u : 0u);
           }
           tc::mma_commit(&sfull[s]);
-          if (one || s == 1) {  // the tile's last use as K
-            tc::mma_commit(&kempty[st]);
-            if (j == t1 - 1) {
-              tc::mma_commit(&qempty[0]);
-              tc::mma_commit(&qempty[1]);
-            }
+        }
+        __syncwarp();
+      };
+      auto wait_k = [&](int j) {
+        const int t = base + j - t0;
+        return wait_warp(&kfull[t % S::kKStages], (t / S::kKStages) & 1);
+      };
+      // tile j has been used as K for the last time (and, with the last tile, the queries)
+      auto release_k = [&](int j) {
+        if (elect_one()) {
+          tc::mma_commit(&kempty[(base + j - t0) % S::kKStages]);
+          if (j == t1 - 1) {
+            tc::mma_commit(&qempty[0]);
+            tc::mma_commit(&qempty[1]);
           }
         }
         __syncwarp();
       };
-      // K of tile j has arrived (awaited once, by the first stream to use it)
-      auto wait_k = [&](int s, int j) {
-        if (!one && s == 1 && j < n0) return true;
-        const int t = base + j - t0;
-        return tc::bar_wait(&kfull[t % S::kKStages], (t / S::kKStages) & 1);
-      };
-      bool first0 = true, first1 = true;
-      // P V of stream s and tile j, then the stream's next scores
-      auto pv = [&](int s, int j, bool& first, int& np) {
-        const int t = base + j - t0, sv = t % S::kVStages;
-        const int jn = one ? j + 2 : j + 1;
-        const bool more_k = jn < t1 && active(one, s, jn, n0);
-        // what arrives early is awaited before the probabilities, so that nothing stands between the two products
-        bool ok = one || s == 0 || j >= n0 ? tc::bar_wait(&vfull[sv], (t / S::kVStages) & 1) : true;
-        if (more_k) ok = ok && wait_k(s, jn);
-        if (clears_tail(one, s, j, n0, L) && lane == 0) bar_arrive(&vland[s]);
-        if (first && items > 0) ok = ok && tc::bar_wait(&oempty[s], (items - 1) & 1);
-        ok = ok && tc::bar_wait(&pfull[s], np & 1);
-        if (!ok) return false;
+      uint32_t fresh = 3;  // streams without a product yet, a bit each
+      // O += P V of half a tile
+      auto pv = [&](int s, int j, int hh, bool last) {
+        const uint32_t first = (fresh >> s) & 1u;
+        if (first && items > 0 && !wait_warp(&oempty[s], (items - 1) & 1)) return false;
+        const uint64_t b =
+            v_desc + __shfl_sync(0xffffffffu, (base + j - t0) % S::kVStages * (S::kVBytes >> 4), 0) + hh * (kStep * 128 >> 4);
+        const uint32_t tP = __shfl_sync(0xffffffffu, tm + s * kTile + hh * (kStep / 2), 0);
+        const uint32_t tD = __shfl_sync(0xffffffffu, tm + 2 * kTile + s * DV, 0);
+        if (!wait_warp(&pfull[2 * s + hh], (parity >> (2 * s + hh)) & 1u)) return false;
         tc::fence_after_sync();
-        const uint64_t b = v_desc + __shfl_sync(0xffffffffu, sv, 0) * (S::kVBytes >> 4);
-        const uint32_t fresh = first ? 0u : 1u;
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_bf16_ts(tm + 2 * kTile + s * DV, tm + s * kTile + k * 8, b + k * (2048 >> 4), id_pv,
-                        k == 0 ? fresh : 1u);
-          tc::mma_commit(&odone[s]);
-          if (one || s == 1) tc::mma_commit(&vempty[sv]);
+          for (int k = 0; k < kStep / 16; ++k)
+            mma_bf16_ts(tD, tP + k * 8, b + k * (2048 >> 4), id_pv, k == 0 ? first ^ 1u : 1u);
+          if (last) tc::mma_commit(&odone[s]);
         }
         __syncwarp();
-        first = false;
-        ++np;
-        if (more_k) qk(s, jn);
+        fresh &= ~(1u << s);
+        parity ^= 1u << (2 * s + hh);
         return true;
       };
-      // the first scores of each stream
-      auto start = [&](int s, int j) {
-        if (j >= t1 || !active(one, s, j, n0) || !wait_k(s, j)) return;
+      // First each stream's first scores (tile t0, or t0 and t0 + 1), then tile by tile the products, each followed
+      // by its stream's next scores.
+      for (int j = one ? t0 - 2 : t0 - 1; j < t1 && healthy; ++j) {
+        const int t = base + j - t0, sv = t % S::kVStages, jn = one ? j + 2 : j + 1;
+        // what arrives early is awaited before the probabilities, so that nothing stands between two products
+        if (j >= t0) healthy = wait_warp(&vfull[sv], (t / S::kVStages) & 1);
+        if (jn < t1) healthy = healthy && wait_k(jn);
         tc::fence_after_sync();
-        qk(s, j);
-      };
-      const int odd = one ? (t0 & 1) : 0;
-      if (odd) {
-        start(1, t0);
-        start(0, t0 + 1);
-      } else {
-        start(0, t0);
-        start(1, one ? t0 + 1 : t0);
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          const int ks = s == 0 ? ks0 : ks1;
+          const int c = j >= t0 ? steps_of(one, s, j, ks) : 0;
+          if (c > 0) bar_arrive_if(&vland[s], lane == 0 && clears_tail(one, s, j, ks0, L));
+#pragma unroll 1
+          for (int hh = 0; hh < c && healthy; ++hh) healthy = pv(s, j, hh, hh + 1 == c);
+          if (jn < t1 && steps_of(one, s, jn, ks) > 0 && healthy) qk(s, jn);
+        }
+        if (jn < t1) release_k(jn);
+        if (j >= t0) {
+          if (elect_one()) tc::mma_commit(&vempty[sv]);
+          __syncwarp();
+        }
       }
-      for (int j = t0; j < t1 && healthy; ++j) {
-        if (active(one, 0, j, n0)) healthy = pv(0, j, first0, np0);
-        if (healthy && active(one, 1, j, n0)) healthy = pv(1, j, first1, np1);
-      }
-      // a stream without a tile here: its previous item's read-out is awaited all the same, so that no
-      // phase of oempty is left two behind
+      // a stream without a tile here: its previous item's read-out is awaited all the same, so that no phase of
+      // oempty is left two behind
       if (items > 0 && healthy) {
-        if (first0) healthy = tc::bar_wait(&oempty[0], (items - 1) & 1);
-        if (first1) healthy = healthy && tc::bar_wait(&oempty[1], (items - 1) & 1);
+        if (fresh & 1u) healthy = wait_warp(&oempty[0], (items - 1) & 1);
+        if (fresh & 2u) healthy = healthy && wait_warp(&oempty[1], (items - 1) & 1);
       }
       base += t1 - t0;
     }
@@ -438,62 +576,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool row_used = rt < g.tpt;
     const float sl2 = p.scale_log2;
     const float step = kRescaleLog2 / sl2;
-    Walk w;
-    bool healthy = true;
+    uint32_t limit = tc::kWaitLimit;  // 1 once a wait has run out: the rest only keeps the barriers in step
     int items = 0, base = 0;
     int ns = 0;     // this stream's tiles so far
-    int tails = 0;  // and those whose V it cleared behind the sequence's end
-    int first_blk = 0, first_s = 0, first_h = 0, flags = 0;
-    for (bool more = w.begin(g, share); more; more = w.next(g), ++items) {
+    int tails = 0;  // those whose V it cleared behind the sequence's end
+    int flags = 0;
+    for (; more; more = w.next(g), ++items) {
       const bool one = w.one;
       const int off = w.q.L - w.q.nq;
-      const int n0 = one ? w.n : (w.blk * g.tpb + g.tpt + off + kTile - 1) / kTile;
+      const int ks0 = stream_keys(g, w, 0), ks = s == 0 ? ks0 : stream_keys(g, w, 1);
       const int tok = w.blk * g.tpb + (one ? 0 : s * g.tpt) + rt;
       const bool valid = row_used && tok < w.q.nq;
       // keys this row sees; a row that is not one is left unmasked (nobody reads its result)
-      int lim = off + tok + 1;
-      if (!valid) lim = 0x7fffffff;
+      const int lim = valid ? off + tok + 1 : 0x7fffffff;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       float m = -INFINITY, l = 0.f;
-      int done = 0;
+      bool any = false;  // a tile done
       for (int j = w.t0; j < w.t1; ++j) {
-        if (!active(one, s, j, n0)) continue;
-        if (healthy) healthy = tc::bar_wait(&sfull[s], ns & 1);
+        const int halves = steps_of(one, s, j, ks);
+        if (halves == 0) continue;
+        if (!wait_warp(&sfull[s], ns & 1, limit)) limit = 1;
         tc::fence_after_sync();
-        const int k0 = j * kTile;
+        float ref = 0.f;
+        const int vis = lim - j * kTile;
+        const bool masked = __any_sync(0xffffffffu, vis < kTile);
         if (warp_valid) {
-          float v[kTile];
+          float mt = -INFINITY;
+#pragma unroll 1
+          for (int hh = 0; hh < halves; ++hh) {
+            float v[kStep];
+            load_scores(v, tS + hh * kStep, masked, vis - hh * kStep);
+            float x0 = max3(v[0], v[1], v[2]), x1 = max3(v[3], v[4], v[5]), x2 = max3(v[6], v[7], v[8]),
+                  x3 = max3(v[9], v[10], v[11]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_async(tS + 32 * c, v + 32 * c);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) fence_regs(v + 32 * c);
-          const int vis = lim - k0;
-          if (__any_sync(0xffffffffu, vis < kTile)) {
-#pragma unroll
-            for (int i = 0; i < kTile; ++i) v[i] = i < vis ? v[i] : -INFINITY;
+            for (int i = 12; i + 8 <= kStep; i += 8) {
+              x0 = max3(x0, v[i], v[i + 1]);
+              x1 = max3(x1, v[i + 2], v[i + 3]);
+              x2 = max3(x2, v[i + 4], v[i + 5]);
+              x3 = max3(x3, v[i + 6], v[i + 7]);
+            }
+            x0 = max3(x0, v[kStep - 4], v[kStep - 3]);
+            x1 = max3(x1, v[kStep - 2], v[kStep - 1]);
+            mt = max3(mt, fmaxf(x0, x1), fmaxf(x2, x3));
           }
-          float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
-#pragma unroll
-          for (int i = 4; i < kTile; i += 4) {
-            x0 = fmaxf(x0, v[i]);
-            x1 = fmaxf(x1, v[i + 1]);
-            x2 = fmaxf(x2, v[i + 2]);
-            x3 = fmaxf(x3, v[i + 3]);
-          }
-          const float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
-          if (done == 0) {
-            m = mt;
-          } else {
-            const bool need = valid && mt > m + step;
-            if (__any_sync(0xffffffffu, need)) {
-              // O and l of the rows that need it move to the new reference; the previous product has to be in
-              if (healthy) healthy = tc::bar_wait(&odone[s], (ns - 1) & 1);
-              tc::fence_after_sync();
-              const float f = need ? exp2_approx((m - mt) * sl2) : 1.f;
-              if (need) m = mt;
-              l *= f;
-#pragma unroll
+          const bool need = valid && mt > m + step;
+          if (__any_sync(0xffffffffu, need)) {
+            // O and l of the rows that need it move to the new reference (from none: by 0); the previous product is
+            // complete, since these scores were issued after it
+            const float f = need ? exp2_approx((m - mt) * sl2) : 1.f;
+            if (need) m = mt;
+            l *= f;
+            if (any) {
+#pragma unroll 1
               for (int c = 0; c < DV / 16; ++c) {
                 float o[16];
                 tmem_ld16(tO + s * DV + 16 * c, o);
@@ -501,68 +635,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 16; ++i) o[i] *= f;
                 tmem_st16(tO + s * DV + 16 * c, o);
               }
-              tc::tmem_wait_st();
             }
           }
-          const float ref = m == -INFINITY ? 0.f : -m * sl2;
-          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float* e = v + 32 * c + 2 * i;
-              fma2(e[0], e[1], e[0], e[1], sl2, ref);
-              fma2(e[2], e[3], e[2], e[3], sl2, ref);
-#pragma unroll
-              for (int u = 0; u < 4; ++u) e[u] = exp2_approx(e[u]);
-              add2(l0, l1, e[0], e[1]);
-              add2(l2, l3, e[2], e[3]);
-              pk[i] = __uint_as_float(pack_bf16x2(e[0], e[1]));
-              pk[i + 1] = __uint_as_float(pack_bf16x2(e[2], e[3]));
-            }
-            tmem_st16(tS + 16 * c, pk);
-          }
-          l += (l0 + l1) + (l2 + l3);
-          tc::tmem_wait_st();
+          ref = m == -INFINITY ? 0.f : -m * sl2;
         }
         // keys past the sequence's end share its last tile: their values may be anything (another sequence,
-        // a page never written), and 0 x NaN is NaN, so those rows of V become zeros.  The MMA thread, which
+        // a page never written), and 0 x NaN is NaN, so those rows of V become zeros.  The MMA warp, which
         // waits for every V tile in turn, says when this one is there.
-        if (clears_tail(one, s, j, n0, w.q.L)) {
-          const int t = base + j - w.t0, sv = t % S::kVStages;
-          if (healthy) healthy = tc::bar_wait(&vland[s], tails & 1);
+        if (clears_tail(one, s, j, ks0, w.q.L)) {
+          if (!wait_warp(&vland[s], tails & 1, limit)) limit = 1;
           ++tails;
-          const int from = w.q.L - k0 > 0 ? w.q.L - k0 : 0;
-          uint8_t* vb = Vs + sv * S::kVBytes;
-          for (int i = r; i < (kTile - from) * 8 * S::kVc; i += kWgThreads) {
-            const int ch = i & 7, row = from + ((i >> 3) % (kTile - from)), c = (i >> 3) / (kTile - from);
-            *reinterpret_cast<uint4*>(vb + c * (kTile * 128) + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
-          }
+          const int from = max(w.q.L - j * kTile, 0), n = (kTile - from) * 8;  // 16-byte pieces per column block
+          uint8_t* vb = Vs + (base + j - w.t0) % S::kVStages * S::kVBytes + from * 128;
+#pragma unroll
+          for (int c = 0; c < S::kVc; ++c)
+            for (int i = r; i < n; i += kWgThreads)
+              *reinterpret_cast<uint4*>(vb + c * (kTile * 128) + i * 16) = make_uint4(0, 0, 0, 0);
           tc::fence_async_smem();
         }
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&pfull[s]);
+#pragma unroll 1
+        for (int hh = 0; hh < halves; ++hh) {
+          if (warp_valid) {
+            float v[kStep];
+            load_scores(v, tS + hh * kStep, masked, vis - hh * kStep);
+            // a masked tile's -inf needs an exact 0, which only the exponential unit gives
+            l += masked ? probabilities<0>(v, sl2, ref, tS + hh * (kStep / 2))
+                        : probabilities<kFmas>(v, sl2, ref, tS + hh * (kStep / 2));
+            tc::tmem_wait_st();
+          }
+          tc::fence_before_sync();
+          __syncwarp();
+          bar_arrive_if(&pfull[2 * s + hh], lane == 0);
+        }
         ++ns;
-        ++done;
+        any = true;
       }
       // ---- epilogue ----
-      if (done > 0) {
-        if (healthy) healthy = tc::bar_wait(&odone[s], (ns - 1) & 1);
-        tc::fence_after_sync();
-      }
       if (items == 0) {
-        first_s = w.s;
-        first_h = w.h;
-        first_blk = w.blk;
+        if (tid == 0) *reinterpret_cast<int3*>(&p.meta[blockIdx.x].y) = make_int3(w.s, w.h, w.blk);
         if (w.t0 > 0 && w.t1 == w.n) flags |= kMetaOwner;
       }
       flags = (flags & kMetaOwner) | (w.t0 == 0 ? kMetaBegins : 0) | (items == 0 ? kMetaSingle : 0);
-      float fa = done > 0 ? 1.f : 0.f, fb = 0.f;
+      if (any) {
+        if (!wait_warp(&odone[s], (ns - 1) & 1, limit)) limit = 1;
+        tc::fence_after_sync();
+      }
       float mr = m == -INFINITY ? -INFINITY : m * sl2;  // log2 units
+      float fa = mr != -INFINITY ? 1.f : 0.f, fb = 0.f;
       if (one) {
-        if (s == 1) stat[r] = make_float2(done > 0 ? mr : -INFINITY, l);
+        if (s == 1) stat[r] = make_float2(mr, l);
         tc::fence_before_sync();
         named_sync(1, 2 * kWgThreads);
         tc::fence_after_sync();
@@ -582,37 +703,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;  // NaN stays NaN
         const int64_t grow = static_cast<int64_t>(w.q.row0 + tok) * p.Hq + w.h * g.G + rg;
         const int64_t prow = (static_cast<int64_t>(2) * blockIdx.x + (items > 0 ? 1 : 0)) * S::kRows + s * kTile + r;
-        const bool read_a = warp_valid && (fa != 0.f || fa != fa), read_b = one && warp_valid && (fb != 0.f || fb != fb);
-        const bool any_a = __any_sync(0xffffffffu, read_a), any_b = __any_sync(0xffffffffu, read_b);
+        fa *= inv;
+        fb *= inv;
+        const bool any_a = __any_sync(0xffffffffu, valid && fa != 0.f), any_b = __any_sync(0xffffffffu, valid && fb != 0.f);
+#pragma unroll 1
+        for (int col = 0; col < DV; col += 16) {
+          float o[16];
 #pragma unroll
-        for (int c = 0; c < DV / 32; ++c) {
-          float o[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          for (int i = 0; i < 16; ++i) o[i] = 0.f;
           if (any_a) {
-            tc::tmem_ld32(tO + s * DV + 32 * c, o);
+            tmem_ld16(tO + s * DV + col, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = read_a ? o[i] * fa : 0.f;
+            for (int i = 0; i < 16; ++i) o[i] = fa != 0.f ? o[i] * fa : 0.f;
           }
           if (any_b) {
-            float o2[32];
-            tc::tmem_ld32(tO + DV + 32 * c, o2);
+            float o2[16];
+            tmem_ld16(tO + DV + col, o2);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] += read_b ? o2[i] * fb : 0.f;
+            for (int i = 0; i < 16; ++i) o[i] += fb != 0.f ? o2[i] * fb : 0.f;
           }
           if (valid) {
             if (whole) {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + grow * DV + 32 * c);
+              uint32_t u[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                dst[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                    pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                    pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                    pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+              for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+              st_global_32(p.out + grow * DV + col, u, p.wide);
             } else {
-              float4* dst = reinterpret_cast<float4*>(p.part + prow * DV + 32 * c);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              float* dst = p.part + prow * DV + col;
+              st_global_32(dst, reinterpret_cast<const uint32_t*>(o), p.wide);
+              st_global_32(dst + 8, reinterpret_cast<const uint32_t*>(o + 8), p.wide);
             }
           }
         }
@@ -629,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       base += w.t1 - w.t0;
     }
-    if (tid == 0) p.meta[blockIdx.x] = make_int4(flags, first_s, first_h, first_blk);
+    if (tid == 0) p.meta[blockIdx.x].x = flags;
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -767,9 +886,9 @@ csa_status run(const char* what, bool paged, Params& p, const gqa::Heads& h, con
   const int64_t max_rows = rows_bound(max_q, h.G);
   const Workspace w = layout(max_rows, h.dv);
   p.Hq = h.Hkv * h.G;
-  p.scale = scale;
   p.scale_log2 = scale * kLog2e;
   p.out = static_cast<__nv_bfloat16*>(out);
+  p.wide = ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(workspace)) & 31u) == 0;
   p.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.part = reinterpret_cast<float*>(ws + w.part);

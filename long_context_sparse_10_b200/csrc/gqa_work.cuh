@@ -7,13 +7,16 @@
 // tokens share a tile and one K/V tile serves all heads of the group.  An item
 // is (sequence, kv head, block of tpb tokens); it needs the key tiles of 128
 // up to its last row's position.  Items are ordered by sequence, kv head and
-// block; CTA c takes the tiles [T c / C, T (c + 1) / C) of the whole list of T,
-// so every CTA has the same number of tiles whatever the lengths are, and an
-// item that straddles a border leaves partial softmax states that a second
-// kernel merges.  The lengths live in device memory (a captured call can be
-// replayed with others), so the kernel computes the partition itself: a closed
-// form counts the tiles of a sequence, and a block-wide sum finds the CTA's
-// first item.
+// block, and each is worth its tiles plus kItemCost for its queries, its
+// read-out and the pipeline's refill (measured at two tiles' time: without it
+// the CTAs whose share was 29 short items of a prompt's first blocks ended 120
+// of 670 us after the others).  CTA c takes the units [U c / C, U (c + 1) / C)
+// of the whole list of U; an item that straddles a border leaves partial
+// softmax states that a second kernel merges.  The lengths live in device
+// memory (a captured call can be replayed with others), so the kernel computes
+// the partition itself: a closed form counts the tiles of a sequence, a
+// block-wide sum finds the sequence of the CTA's first unit, and one thread
+// its block.
 #pragma once
 
 #include "common.cuh"
@@ -22,6 +25,7 @@ namespace csa {
 namespace gqa {
 
 constexpr int kTile = 128;  // keys per tile, and rows per tile
+constexpr int kItemCost = 2;
 
 struct Geometry {
   const int32_t* cu_q;       // [n_seqs + 1]
@@ -34,25 +38,27 @@ struct Geometry {
   int tpb;                   // tokens per item (one or two tiles)
 };
 
-// sum_{t < n} floor((a t + b) / m) for n, a, b >= 0, m > 0, in O(log) steps:
-// whole parts come out, and what is left is the same sum with the roles of
-// the axes exchanged (lattice points under the line).
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// sum_{t < n} floor((a t + b) / m) for a n + b < 2^32, in O(log) steps: whole
+// parts come out, and what is left is the same sum with the roles of the axes
+// exchanged (lattice points under the line).
+__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t ans = 0;
   while (n > 0) {
     if (a >= m) {
-      ans += n * (n - 1) / 2 * (a / m);
-      a %= m;
+      const uint32_t q = a / m;
+      ans += static_cast<int64_t>(n) * (n - 1) / 2 * q;
+      a -= q * m;
     }
     if (b >= m) {
-      ans += n * (b / m);
-      b %= m;
+      const uint32_t q = b / m;
+      ans += static_cast<int64_t>(n) * q;
+      b -= q * m;
     }
-    const int64_t y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
-    b = y % m;
-    const int64_t t = m;
+    b = y - n * m;
+    const uint32_t t = m;
     m = a;
     a = t;
   }
@@ -98,17 +104,19 @@ struct Seq {
     sum += z;
     // block z + t: floor((off + 127 + (z + 1) tpb + t tpb) / 128)
     if (n > z)
-      sum += floor_sum(n - z, kTile, g.tpb, static_cast<int64_t>(off) + kTile - 1 + static_cast<int64_t>(z + 1) * g.tpb);
+      sum += floor_sum(static_cast<uint32_t>(n - z), kTile, static_cast<uint32_t>(g.tpb),
+                       static_cast<uint32_t>(off + kTile - 1 + (z + 1) * g.tpb));
     return sum;
+  }
+  __device__ __forceinline__ int64_t units_before(const Geometry& g, int n) const {
+    return tiles_before(g, n) + static_cast<int64_t>(n) * kItemCost;
   }
 };
 
-// What one CTA does: tiles [start, start + left) of the list, beginning in
-// sequence s at tile `within` of that sequence's Hkv * tiles_before(nblk).
+// What one CTA does: `left` units of the list, beginning at unit `unit` of an
+// item.
 struct Share {
-  int64_t left, within;
-  int s;
-  int ctas;  // CTAs that have work
+  int left, s, h, blk, unit;
 };
 
 // All threads of the block call this (blockDim.x a multiple of 32, at most
@@ -121,7 +129,7 @@ __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ct
   for (int s = s0; s < s1; ++s) {
     Seq q;
     q.load(g, s);
-    mine += q.tiles_before(g, q.nblk) * g.Hkv;
+    mine += q.units_before(g, q.nblk) * g.Hkv;
   }
   int64_t inc = mine;
 #pragma unroll
@@ -130,10 +138,6 @@ __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ct
     if (lane >= o) inc += v;
   }
   if (lane == 31) scratch[warp] = inc;
-  if (tid == 0) {
-    scratch[32] = -1;
-    scratch[33] = 0;
-  }
   __syncthreads();
   int64_t before = 0, total = 0;
   for (int w = 0; w < nw; ++w) {
@@ -142,67 +146,86 @@ __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ct
     total += v;
   }
   before += inc - mine;
-  Share sh;
-  sh.ctas = static_cast<int>(total < n_ctas ? total : n_ctas);
-  sh.left = 0;
-  sh.within = 0;
-  sh.s = 0;
-  if (cta >= sh.ctas) return sh;  // the same for every thread of the block
-  const int64_t start = total * cta / sh.ctas, end = total * (cta + 1) / sh.ctas;
-  sh.left = end - start;
+  const int ctas = static_cast<int>(total < n_ctas ? total : n_ctas);
+  Share sh = {0, 0, 0, 0, 0};
+  if (cta >= ctas) return sh;  // the same for every thread of the block
+  const int64_t per = total / ctas, more = total - per * ctas;  // the first `more` CTAs take one unit more
+  const int64_t start = per * cta + (cta < more ? cta : more);
+  sh.left = static_cast<int>(per + (cta < more ? 1 : 0));
   if (start >= before && start < before + mine) {
-    int64_t at = before;
-    for (int s = s0; s < s1; ++s) {
-      Seq q;
-      q.load(g, s);
-      const int64_t n = q.tiles_before(g, q.nblk) * g.Hkv;
-      if (start < at + n) {
-        scratch[32] = s;
-        scratch[33] = start - at;
-        break;
-      }
-      at += n;
+    int64_t at = start - before;
+    int s = s0;
+    Seq q;
+    q.load(g, s);
+    int64_t seq = q.units_before(g, q.nblk);
+    while (at >= seq * g.Hkv) {
+      at -= seq * g.Hkv;
+      q.load(g, ++s);
+      seq = q.units_before(g, q.nblk);
+    }
+    const int h = static_cast<int>((at >> 32) ? at / seq : static_cast<uint32_t>(at) / static_cast<uint32_t>(seq));
+    at -= h * seq;
+    scratch[34] = at;
+    int32_t* out = reinterpret_cast<int32_t*>(scratch + 32);
+    out[0] = s;
+    out[1] = h;
+  }
+  __syncthreads();
+  if (warp == 0) {  // the last block with units_before <= at, 32 candidates at a time
+    int32_t* out = reinterpret_cast<int32_t*>(scratch + 32);
+    const int64_t at = scratch[34];
+    Seq q;
+    q.load(g, out[0]);
+    int lo = 0, n = q.nblk;  // it is in [lo, lo + n)
+    while (n > 1) {
+      const int gap = (n + 31) / 32;
+      const bool here = lane * gap < n && q.units_before(g, lo + lane * gap) <= at;
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, here));
+      n = min(gap, n - k * gap);
+      lo += k * gap;
+    }
+    if (lane == 0) {
+      out[2] = lo;
+      out[3] = static_cast<int>(at - q.units_before(g, lo));
     }
   }
   __syncthreads();
-  sh.s = static_cast<int>(scratch[32]);
-  sh.within = scratch[33];
+  const int32_t* out = reinterpret_cast<const int32_t*>(scratch + 32);
+  sh.s = out[0];
+  sh.h = out[1];
+  sh.blk = out[2];
+  sh.unit = out[3];
   return sh;
 }
 
-// Walks a share item by item.
+// Walks a share item by item, over the pieces that have a tile.
 struct Walk {
   Seq q;
   int s, h, blk;
   int t0, t1, n;  // this piece's key tiles [t0, t1) of the item's n
-  int left;       // tiles of the share from this piece on
+  int left;       // units of the share behind this piece
   bool one;       // the block's rows fit one 128-row tile
 
-  __device__ __forceinline__ void set(const Geometry& g, int ta) {
+  // the piece from unit u of the current item; false where it has no tile
+  __device__ __forceinline__ bool set(const Geometry& g, int u) {
     n = q.tiles(g, blk);
-    t0 = ta;
-    t1 = ta + min(n - ta, left);
+    const int end = min(kItemCost + n, u + left);
+    left -= end - u;
+    t0 = max(u - kItemCost, 0);
+    t1 = max(end - kItemCost, 0);
     one = g.tpb <= g.tpt || q.nq - blk * g.tpb <= g.tpt;
+    return t1 > t0;
   }
   __device__ __forceinline__ bool begin(const Geometry& g, const Share& sh) {
-    left = static_cast<int>(sh.left);
+    left = sh.left;
     if (left <= 0) return false;
     s = sh.s;
+    h = sh.h;
+    blk = sh.blk;
     q.load(g, s);
-    const int64_t per = q.tiles_before(g, q.nblk);
-    h = static_cast<int>(sh.within / per);
-    const int64_t r = sh.within - h * per;
-    int lo = 0, hi = q.nblk - 1;  // the last block with tiles_before <= r
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (q.tiles_before(g, mid) <= r) lo = mid; else hi = mid - 1;
-    }
-    blk = lo;
-    set(g, static_cast<int>(r - q.tiles_before(g, lo)));
-    return true;
+    return set(g, sh.unit) || next(g);
   }
   __device__ __forceinline__ bool next(const Geometry& g) {
-    left -= t1 - t0;
     if (left <= 0) return false;
     if (++blk >= q.nblk) {
       blk = 0;
@@ -214,8 +237,7 @@ struct Walk {
         } while (q.nblk == 0);
       }
     }
-    set(g, 0);
-    return true;
+    return set(g, 0);  // without a tile only where the share ends in the item's cost
   }
   __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
 };
