@@ -13,10 +13,11 @@
 //                   scores read from TMEM, one pass with a running reference
 //                   and sum, probabilities written back to TMEM as bf16
 //   warp 8          TMA producer (128-byte swizzled K and V tiles, rings)
-//   warp 9          issues the MMAs: S = Q K^T (both operands in
-//                   shared memory), O += P V (P from TMEM, V as it lies in
-//                   memory, channel-major for the MMA)
-//   warps 10, 11    none (they complete the warpgroup whose registers move)
+//   warps 9, 10     issue the MMAs of one stream each, so that neither waits
+//                   for the other's softmax: S = Q K^T (both operands in shared
+//                   memory), O += P V (P from TMEM, V as it lies in memory,
+//                   channel-major for the MMA)
+//   warp 11         none (it completes the warpgroup whose registers move)
 // Two streams keep the tensor core busy while the other stream is in its
 // softmax.  An item of two 128-row tiles gives one tile to each stream, and
 // both read the same K/V tile; an item of at most one tile (decode) gives its
@@ -358,15 +359,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < S::kKStages; ++i) {
       tc::bar_init(&kfull[i], 1);
-      tc::bar_init(&kempty[i], 1);
+      tc::bar_init(&kempty[i], 2);
     }
     for (int i = 0; i < S::kVStages; ++i) {
       tc::bar_init(&vfull[i], 1);
-      tc::bar_init(&vempty[i], 1);
+      tc::bar_init(&vempty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       tc::bar_init(&qfull[i], 1);
-      tc::bar_init(&qempty[i], 1);
+      tc::bar_init(&qempty[i], 2);
       tc::bar_init(&sfull[i], 1);
       tc::bar_init(&pfull[2 * i], 4);
       tc::bar_init(&pfull[2 * i + 1], 4);
@@ -456,114 +457,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         row_cur = row_next;
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 9 || warp == 10) {
     regs_down();
-    // ===================== MMA issue (the whole warp walks, one lane issues) =====================
-    // The operands of an MMA are uniform registers: the warp stays converged and descriptors advance by
-    // constants, so that issuing eight of them takes less time than the tensor core needs for one.
+    // ===================== MMA issue (a warp per stream walks, one lane issues) =====================
+    // The operands of an MMA are uniform registers: the warp stays converged and descriptors advance by constants.
     constexpr uint32_t id_qk = tc::idesc_bf16(kTile, kTile, false, false);
     constexpr uint32_t id_pv = tc::idesc_bf16(kTile, DV, true, false);
+    const int s = __shfl_sync(0xffffffffu, warp - 9, 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t tS = tm + s * kTile, tO = tm + 2 * kTile + s * DV;
     const uint64_t q_desc = tc::desc_sw128(smem_u32(Qs), 16, 1024), k_desc = tc::desc_sw128(smem_u32(Ks), 16, 1024);
     const uint64_t v_desc = tc::desc_sw128(smem_u32(Vs), kTile * 128, 1024);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     bool healthy = true;
     int items = 0, pairs = 0;
-    int base = 0;                                       // this CTA's tiles before the item
-    uint32_t parity = 0;                                // of pfull[stream][half], a bit each
+    int base = 0;             // this CTA's tiles before the item
+    uint32_t parity = 0;      // of pfull[s][half], a bit each
     for (; more && healthy; more = w.next(g), ++items) {
       const bool one = w.one;
-      const int t0 = w.t0, t1 = w.t1, L = w.q.L;
-      const int ks0 = stream_keys(g, w, 0), ks1 = stream_keys(g, w, 1);
-      healthy = wait_warp(&qfull[0], items & 1);
-      if (!one) {
-        healthy = healthy && wait_warp(&qfull[1], pairs & 1);
-        ++pairs;
-      }
-      // S = Q K^T of a tile
-      auto qk = [&](int s, int j) {
-        const int st = (base + j - t0) % S::kKStages;
-        const uint64_t a = q_desc + __shfl_sync(0xffffffffu, one ? 0 : s * (S::kQBytes >> 4), 0);
+      const int t0 = w.t0, t1 = w.t1;
+      const int ks0 = stream_keys(g, w, 0), ks = s == 0 ? ks0 : stream_keys(g, w, 1);
+      // its queries: tile s, or the one tile there is
+      healthy = s == 0 || one ? wait_warp(&qfull[0], items & 1) : wait_warp(&qfull[1], pairs & 1);
+      pairs += one ? 0 : 1;
+      const uint64_t qd = q_desc + (one ? 0 : __shfl_sync(0xffffffffu, s * (S::kQBytes >> 4), 0));
+      // The stream's scores of tile j, and word that it is done with the tile as K (with the last one, with the
+      // queries too).  Every tile's word comes from both streams, after the tile has arrived.
+      auto scores = [&](int j) {
+        const int t = base + j - t0, st = t % S::kKStages;
+        if (!wait_warp(&kfull[st], (t / S::kKStages) & 1)) return false;
+        const bool mine = steps_of(one, s, j, ks) > 0;
         const uint64_t b = k_desc + __shfl_sync(0xffffffffu, st * (S::kQBytes >> 4), 0);
-        const uint32_t d = __shfl_sync(0xffffffffu, tm + s * kTile, 0);
+        tc::fence_after_sync();
         if (elect_one()) {
+          if (mine) {
 #pragma unroll
-          for (int k = 0; k < DQK / 16; ++k) {
-            const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;  // descriptors count 16-byte units
-            tc::mma_bf16_ss(d, a + o, b + o, id_qk, k != 0 ? 1u : 0u);
+            for (int k = 0; k < DQK / 16; ++k) {
+              const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;  // descriptors count 16-byte units
+              tc::mma_bf16_ss(tS, qd + o, b + o, id_qk, k != 0 ? 1u : 0u);
+            }
+            tc::mma_commit(&sfull[s]);
           }
-          tc::mma_commit(&sfull[s]);
-        }
-        __syncwarp();
-      };
-      auto wait_k = [&](int j) {
-        const int t = base + j - t0;
-        return wait_warp(&kfull[t % S::kKStages], (t / S::kKStages) & 1);
-      };
-      // tile j has been used as K for the last time (and, with the last tile, the queries)
-      auto release_k = [&](int j) {
-        if (elect_one()) {
-          tc::mma_commit(&kempty[(base + j - t0) % S::kKStages]);
+          tc::mma_commit(&kempty[st]);
           if (j == t1 - 1) {
             tc::mma_commit(&qempty[0]);
             tc::mma_commit(&qempty[1]);
           }
         }
         __syncwarp();
-      };
-      uint32_t fresh = 3;  // streams without a product yet, a bit each
-      // O += P V of half a tile
-      auto pv = [&](int s, int j, int hh, bool last) {
-        const uint32_t first = (fresh >> s) & 1u;
-        if (first && items > 0 && !wait_warp(&oempty[s], (items - 1) & 1)) return false;
-        const uint64_t b =
-            v_desc + __shfl_sync(0xffffffffu, (base + j - t0) % S::kVStages * (S::kVBytes >> 4), 0) + hh * (kStep * 128 >> 4);
-        const uint32_t tP = __shfl_sync(0xffffffffu, tm + s * kTile + hh * (kStep / 2), 0);
-        const uint32_t tD = __shfl_sync(0xffffffffu, tm + 2 * kTile + s * DV, 0);
-        if (!wait_warp(&pfull[2 * s + hh], (parity >> (2 * s + hh)) & 1u)) return false;
-        tc::fence_after_sync();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kStep / 16; ++k)
-            mma_bf16_ts(tD, tP + k * 8, b + k * (2048 >> 4), id_pv, k == 0 ? first ^ 1u : 1u);
-          if (last) tc::mma_commit(&odone[s]);
-        }
-        __syncwarp();
-        fresh &= ~(1u << s);
-        parity ^= 1u << (2 * s + hh);
         return true;
       };
-      // First each stream's first scores (tile t0, or t0 and t0 + 1), then tile by tile the products, each followed
-      // by its stream's next scores.
-      for (int j = one ? t0 - 2 : t0 - 1; j < t1 && healthy; ++j) {
-        const int t = base + j - t0, sv = t % S::kVStages, jn = one ? j + 2 : j + 1;
-        // what arrives early is awaited before the probabilities, so that nothing stands between two products
-        if (j >= t0) healthy = wait_warp(&vfull[sv], (t / S::kVStages) & 1);
-        if (jn < t1) healthy = healthy && wait_k(jn);
-        tc::fence_after_sync();
-#pragma unroll 1
-        for (int s = 0; s < 2; ++s) {
-          const int ks = s == 0 ? ks0 : ks1;
-          const int c = j >= t0 ? steps_of(one, s, j, ks) : 0;
-          if (c > 0) bar_arrive_if(&vland[s], lane == 0 && clears_tail(one, s, j, ks0, L));
-#pragma unroll 1
-          for (int hh = 0; hh < c && healthy; ++hh) healthy = pv(s, j, hh, hh + 1 == c);
-          if (jn < t1 && steps_of(one, s, jn, ks) > 0 && healthy) qk(s, jn);
-        }
-        if (jn < t1) release_k(jn);
+      bool fresh = true;  // no product yet
+      const int ahead = one ? 2 : 1;
+      // Tile by tile the products, each followed by the stream's next scores (those of its first tile come first).
+      for (int j = t0 - ahead; j < t1 && healthy; ++j) {
+        const int jn = j + ahead;
         if (j >= t0) {
+          const int t = base + j - t0, sv = t % S::kVStages, c = steps_of(one, s, j, ks);
+          healthy = wait_warp(&vfull[sv], (t / S::kVStages) & 1);
+          bar_arrive_if(&vland[s], lane == 0 && c > 0 && clears_tail(one, s, j, ks0, w.q.L));
+          if (c > 0 && fresh && items > 0) healthy = healthy && wait_warp(&oempty[s], (items - 1) & 1);
+          const uint64_t vd = v_desc + __shfl_sync(0xffffffffu, sv * (S::kVBytes >> 4), 0);
+#pragma unroll 1
+          for (int hh = 0; hh < c && healthy; ++hh) {
+            const uint64_t b = vd + hh * (kStep * 128 >> 4);
+            const uint32_t tP = tS + hh * (kStep / 2), add = fresh ? 0u : 1u;
+            healthy = wait_warp(&pfull[2 * s + hh], (parity >> hh) & 1u);
+            if (!healthy) break;
+            tc::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kStep / 16; ++k) mma_bf16_ts(tO, tP + k * 8, b + k * (2048 >> 4), id_pv, k == 0 ? add : 1u);
+              if (hh + 1 == c) tc::mma_commit(&odone[s]);
+            }
+            __syncwarp();
+            fresh = false;
+            parity ^= 1u << hh;
+          }
+          if (healthy && jn < t1) healthy = scores(jn);
           if (elect_one()) tc::mma_commit(&vempty[sv]);
           __syncwarp();
+        } else if (jn < t1) {
+          healthy = scores(jn);
         }
       }
       // a stream without a tile here: its previous item's read-out is awaited all the same, so that no phase of
       // oempty is left two behind
-      if (items > 0 && healthy) {
-        if (fresh & 1u) healthy = wait_warp(&oempty[0], (items - 1) & 1);
-        if (fresh & 2u) healthy = healthy && wait_warp(&oempty[1], (items - 1) & 1);
-      }
+      if (items > 0 && healthy && fresh) healthy = wait_warp(&oempty[s], (items - 1) & 1);
       base += t1 - t0;
     }
-  } else if (warp >= 10) {
+  } else if (warp == 11) {
     regs_down();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
