@@ -2196,7 +2196,8 @@ csa_status csa_check_device_error(void* stream) {
   e = cudaMemcpyFromSymbol(&word, csa::tc::g_device_error, sizeof(int));
   if (e != cudaSuccess) return csa::fail(CSA_ERR_CUDA, "csa_check_device_error: %s", cudaGetErrorString(e));
   for (int (*reader)(bool) : {csa::indexer_device_error, csa::compress_device_error, csa::out_proj_device_error,
-                               csa::cp_merge_device_error, csa::gqa_device_error, csa::gqa_cache_device_error}) {
+                               csa::cp_merge_device_error, csa::gqa_device_error, csa::gqa_cache_device_error,
+                               csa::gqa_mass_device_error}) {
     const int uword = reader(true);
     if (uword < 0) return csa::fail(CSA_ERR_CUDA, "csa_check_device_error: cannot read a unit's error word");
     word |= uword;

@@ -42,6 +42,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "gqa_device.cuh"
 #include "gqa_host.h"
 #include "gqa_work.cuh"
 #include "host_util.h"
@@ -50,10 +51,7 @@
 namespace csa {
 namespace {
 
-using gqa::Geometry;
-using gqa::kTile;
-using gqa::Seq;
-using gqa::Walk;
+using namespace gqa;
 
 constexpr int kThreads = 384;
 // Registers: 384 threads start with 168 each; the softmax warpgroups take more (a row of scores is 128 of them)
@@ -102,116 +100,6 @@ struct Params {
 constexpr int kMetaOwner = 1;   // the first piece ends its item and does not begin it: this CTA's merge
 constexpr int kMetaBegins = 2;  // the last piece begins its item
 constexpr int kMetaSingle = 4;  // the last piece is the first
-
-// D(TMEM) += A(TMEM, bf16 pairs) * B(shared)
-__device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
-}
-
-// 32 columns without a wait; fence_regs() after the wait keeps uses behind it.
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
-          taddr),
-      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
-      : "memory");
-}
-__device__ __forceinline__ void fence_regs(float* v) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), "+f"(v[i + 5]),
-                      "+f"(v[i + 6]), "+f"(v[i + 7]));
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Two fp32 operations in one instruction (each rounded as its scalar form).
-__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
-  asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %4};\nmov.b64 c, {%5, %5};\n"
-      "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b), "f"(c));
-}
-__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
-  asm("{\n.reg .b64 a, d;\nmov.b64 a, {%2, %3};\nmov.b64 d, {%0, %1};\nadd.rn.f32x2 d, d, a;\n"
-      "mov.b64 {%0, %1}, d;\n}\n"
-      : "+f"(d0), "+f"(d1)
-      : "f"(a0), "f"(a1));
-}
-
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
-// Wait of a converged warp for a barrier's phase.  Almost always the phase is there or arrives within one try: that
-// path has one try and a vote, so that no branch of it diverges (a loop whose exit is each lane's own costs 150
-// clocks more).  The bounded loop is for the rest; false, for all lanes, when it runs out.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t limit = tc::kWaitLimit) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  bool all = __all_sync(0xffffffffu, ok != 0);
-  if (!all) all = __all_sync(0xffffffffu, tc::bar_wait_bounded(bar, parity, limit));
-  return all;
-}
-// Arrives where `on` holds, without a branch.
-__device__ __forceinline__ void bar_arrive_if(uint64_t* bar, bool on, uint32_t n = 1) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 _, [%0], %2;\n}\n" ::"r"(
-                   smem_u32(bar)),
-               "r"(static_cast<uint32_t>(on)), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-// 32 bytes in one store where the address allows it: a warp whose lanes write 32 different rows pays per row.
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
-}
-__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) { tc::bar_arrive_expect_tx(bar, bytes); }
-__device__ __forceinline__ void named_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
-}
 
 // (a0, a1) + (b, b) and (a0, a1) * (b0, b1) + (c, c), as above.
 __device__ __forceinline__ void add2s(float& d0, float& d1, float a0, float a1, float b) {
@@ -285,13 +173,6 @@ __device__ __forceinline__ float probabilities(float* v, float a, float b, uint3
     tmem_st16(tP + 16 * c, pk);
   }
   return (l0 + l1) + (l2 + l3);
-}
-
-// One lane of a converged warp (always the same one).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
-  return r != 0;
 }
 
 __device__ __forceinline__ void regs_down() {
@@ -378,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::bar_init_fence();
   }
   if (warp == 9) tc::tmem_alloc(tslot, 512);
-  const gqa::Share share = gqa::find_share(g, blockIdx.x, gridDim.x, scratch);
+  const gqa::Share share = gqa::find_share<gqa::Blocks>(g, blockIdx.x, gridDim.x, scratch);
   Walk w;
   bool more = w.begin(g, share);
   tc::fence_before_sync();

@@ -1,33 +1,12 @@
-// The paged cache of the grouped-head (GQA) attention: appending a chunk,
-// accumulating the attention weight of cached tokens, and eviction by it.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "common.cuh"
+// The paged cache of the grouped-head (GQA) attention: appending a chunk, and
+// eviction by accumulated weight.
+#include "gqa_device.cuh"
 #include "gqa_host.h"
-#include "gqa_work.cuh"
-#include "host_util.h"
 
 namespace csa {
 namespace {
 
-// A pool of pages and one table of them.
-struct Pool {
-  uint4* k;  // 16-byte pieces
-  uint4* v;
-  float* mass;
-  int64_t n_pages;
-  int Hkv, page, kp, vp;  // kp, vp: pieces per token of k and v
-};
-
-// Slot (row of the pool's planes) of a position, or -1 where the table holds no page of the pool for it.
-__device__ __forceinline__ int64_t slot_of(const Pool& c, const int32_t* table, int max_pages, int h, int pos) {
-  const int pg = pos / c.page;
-  if (pos < 0 || pg >= max_pages) return -1;
-  const int id = __ldg(table + pg);
-  if (id < 0 || id >= c.n_pages) return -1;
-  return (static_cast<int64_t>(id) * c.Hkv + h) * c.page + pos % c.page;
-}
+using namespace gqa;
 
 // ---------------------------------------------------------------------------
 // Append: a warp per new token copies its rows of all kv heads, 16 bytes a
@@ -65,54 +44,6 @@ __global__ void __launch_bounds__(256) gqa_append_kernel(const __grid_constant__
   }
   if (p.c.mass != nullptr)
     for (int h = lane; h < p.c.Hkv; h += 32) p.c.mass[at + h * step] = 0.f;
-}
-
-// ---------------------------------------------------------------------------
-// Accumulated weight: a warp per cached token and kv head, one dot product per
-// row that sees it.
-// ---------------------------------------------------------------------------
-struct MassParams {
-  Pool c;
-  gqa::Geometry g;
-  const __nv_bfloat16* q;
-  const float* lse;
-  const int32_t* block_table;
-  int max_pages;
-  float scale_log2;
-};
-
-template <int DQK>
-__global__ void __launch_bounds__(256) gqa_mass_kernel(const __grid_constant__ MassParams p) {
-  pdl_wait();
-  constexpr int kPer = DQK / 32;
-  const int lane = threadIdx.x & 31, h = blockIdx.y, s = blockIdx.z;
-  gqa::Seq q;
-  q.load(p.g, s);
-  const int off = q.L - q.nq;
-  const __nv_bfloat16* kp = reinterpret_cast<const __nv_bfloat16*>(p.c.k);
-  for (int u = threadIdx.x >> 5; u < 64; u += 8) {
-    const int j = blockIdx.x * 64 + u;
-    if (j >= q.L) return;
-    const int64_t at = slot_of(p.c, p.block_table + static_cast<int64_t>(s) * p.max_pages, p.max_pages, h, j);
-    if (at < 0) continue;
-    float kv[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) kv[i] = __bfloat162float(kp[at * DQK + lane * kPer + i]);
-    float sum = 0.f;
-    for (int i = max(0, j - off); i < q.nq; ++i) {
-      for (int g = 0; g < p.g.G; ++g) {
-        const int64_t r = (static_cast<int64_t>(q.row0) + i) * p.g.Hkv * p.g.G + h * p.g.G + g;
-        float d = 0.f;
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) d += kv[x] * __bfloat162float(p.q[r * DQK + lane * kPer + x]);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        const float l = p.lse[r];
-        if (l != -INFINITY) sum += exp2f(d * p.scale_log2 - l * kLog2e);
-      }
-    }
-    if (lane == 0) p.c.mass[at] += sum;
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -261,19 +192,6 @@ __global__ void __launch_bounds__(256) gqa_evict_gather_kernel(const __grid_cons
   }
 }
 
-Pool pool_of(const gqa_cache* c) {
-  Pool p;
-  p.k = static_cast<uint4*>(c->k);
-  p.v = static_cast<uint4*>(c->v);
-  p.mass = c->mass;
-  p.n_pages = c->n_pages;
-  p.Hkv = c->n_kv_heads;
-  p.page = c->page_size;
-  p.kp = c->d_qk / 8;
-  p.vp = c->d_v / 8;
-  return p;
-}
-
 }  // namespace
 }  // namespace csa
 
@@ -304,47 +222,6 @@ csa_status gqa_cache_append(const void* k, const void* v, const gqa_cache* cache
   const unsigned blocks = static_cast<unsigned>((batch->total_q + 7) / 8);
   prof_begin(s);
   const cudaError_t e = launch_pdl(gqa_append_kernel, dim3(blocks), dim3(256), 0, s, 1, p);
-  prof_end(s);
-  return check_launch(what, e);
-}
-
-csa_status gqa_cache_mass(const void* q, const float* lse, const gqa_cache* cache, const gqa_batch* batch, int32_t H,
-                          float scale, void* stream) {
-  using namespace csa;
-  const char* what = "gqa_cache_mass";
-  clear_error();
-  gqa::Heads h;
-  if (csa_status st = gqa::check_paged(what, cache, batch, H, &h); st != CSA_OK) return st;
-  if (csa_status st = gqa::check_scale(what, scale); st != CSA_OK) return st;
-  CSA_REQUIRE(cache->mass != nullptr, "%s: the cache has no mass plane", what);
-  if (batch->n_seqs == 0 || batch->total_q == 0) return CSA_OK;
-  if (csa_status st = gqa::check_pool(what, cache, batch, true); st != CSA_OK) return st;
-  CSA_REQUIRE_PTR(q);
-  CSA_REQUIRE_PTR(lse);
-  CSA_REQUIRE_PTR(cache->mass);
-  CSA_REQUIRE(batch->n_seqs <= 65535, "%s: at most 65535 sequences", what);
-  MassParams p;
-  memset(&p, 0, sizeof(p));
-  p.c = pool_of(cache);
-  p.g.cu_q = batch->cu_q;
-  p.g.cache_len = batch->cache_len;
-  p.g.n_seqs = batch->n_seqs;
-  p.g.max_len = gqa::max_len(cache, batch);
-  p.g.total_q = batch->total_q;
-  p.g.Hkv = h.Hkv;
-  p.g.G = h.G;
-  p.g.tpt = p.g.tpb = 1;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.lse = lse;
-  p.block_table = batch->block_table;
-  p.max_pages = batch->max_pages;
-  p.scale_log2 = scale * kLog2e;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid((p.g.max_len + 63) / 64, h.Hkv, batch->n_seqs);
-  prof_begin(s);
-  cudaError_t e = h.dqk == 192   ? launch_pdl(gqa_mass_kernel<192>, grid, dim3(256), 0, s, 1, p)
-                  : h.dqk == 128 ? launch_pdl(gqa_mass_kernel<128>, grid, dim3(256), 0, s, 1, p)
-                                 : launch_pdl(gqa_mass_kernel<64>, grid, dim3(256), 0, s, 1, p);
   prof_end(s);
   return check_launch(what, e);
 }

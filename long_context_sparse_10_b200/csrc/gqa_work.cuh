@@ -15,8 +15,8 @@
 // softmax states that a second kernel merges.  The lengths live in device
 // memory (a captured call can be replayed with others), so the kernel computes
 // the partition itself: a closed form counts the tiles of a sequence, a
-// block-wide sum finds the sequence of the CTA's first unit, and one thread
-// its block.
+// block-wide sum finds the sequence of the CTA's first unit, and a warp its
+// block.
 #pragma once
 
 #include "common.cuh"
@@ -108,9 +108,6 @@ struct Seq {
                        static_cast<uint32_t>(off + kTile - 1 + (z + 1) * g.tpb));
     return sum;
   }
-  __device__ __forceinline__ int64_t units_before(const Geometry& g, int n) const {
-    return tiles_before(g, n) + static_cast<int64_t>(n) * kItemCost;
-  }
 };
 
 // What one CTA does: `left` units of the list, beginning at unit `unit` of an
@@ -119,8 +116,37 @@ struct Share {
   int left, s, h, blk, unit;
 };
 
+// The attention's items of a sequence: its row blocks.
+struct Blocks {
+  static __device__ __forceinline__ int count(const Seq& q) { return q.nblk; }
+  static __device__ __forceinline__ int64_t units_before(const Geometry& g, const Seq& q, int n) {
+    return q.tiles_before(g, n) + static_cast<int64_t>(n) * kItemCost;
+  }
+};
+
+// The accumulated weight's items: pairs of key tiles, each worth kItemCost and
+// the row blocks (of tpb = tpt tokens) with a row that sees the pair's first key.
+struct KeyPairs {
+  static __device__ __forceinline__ int count(const Seq& q) { return q.nq > 0 ? (q.L + 2 * kTile - 1) / (2 * kTile) : 0; }
+  static __device__ __forceinline__ int first_block(const Geometry& g, const Seq& q, int pair) {
+    const int t = pair * 2 * kTile - (q.L - q.nq);  // the first row that sees the key
+    return t <= 0 ? 0 : t / g.tpb;
+  }
+  static __device__ __forceinline__ int64_t units_before(const Geometry& g, const Seq& q, int n) {
+    const int off = q.L - q.nq;
+    int z = off < 0 ? 0 : off / (2 * kTile) + 1;  // pairs that every block sees
+    z = z < n ? z : n;
+    int64_t units = static_cast<int64_t>(n) * (q.nblk + kItemCost);
+    if (n > z)
+      units -= floor_sum(static_cast<uint32_t>(n - z), static_cast<uint32_t>(g.tpb), 2 * kTile,
+                         static_cast<uint32_t>(z * 2 * kTile - off));
+    return units;
+  }
+};
+
 // All threads of the block call this (blockDim.x a multiple of 32, at most
 // 1024); `scratch` holds 40 int64 words.
+template <typename Items>
 __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ctas, int64_t* scratch) {
   const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nthr >> 5;
   const int chunk = (g.n_seqs + nthr - 1) / nthr;
@@ -129,7 +155,7 @@ __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ct
   for (int s = s0; s < s1; ++s) {
     Seq q;
     q.load(g, s);
-    mine += q.units_before(g, q.nblk) * g.Hkv;
+    mine += Items::units_before(g, q, Items::count(q)) * g.Hkv;
   }
   int64_t inc = mine;
 #pragma unroll
@@ -157,11 +183,11 @@ __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ct
     int s = s0;
     Seq q;
     q.load(g, s);
-    int64_t seq = q.units_before(g, q.nblk);
+    int64_t seq = Items::units_before(g, q, Items::count(q));
     while (at >= seq * g.Hkv) {
       at -= seq * g.Hkv;
       q.load(g, ++s);
-      seq = q.units_before(g, q.nblk);
+      seq = Items::units_before(g, q, Items::count(q));
     }
     const int h = static_cast<int>((at >> 32) ? at / seq : static_cast<uint32_t>(at) / static_cast<uint32_t>(seq));
     at -= h * seq;
@@ -171,22 +197,22 @@ __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ct
     out[1] = h;
   }
   __syncthreads();
-  if (warp == 0) {  // the last block with units_before <= at, 32 candidates at a time
+  if (warp == 0) {  // the last item of the head with units_before <= at, 32 candidates at a time
     int32_t* out = reinterpret_cast<int32_t*>(scratch + 32);
     const int64_t at = scratch[34];
     Seq q;
     q.load(g, out[0]);
-    int lo = 0, n = q.nblk;  // it is in [lo, lo + n)
+    int lo = 0, n = Items::count(q);  // it is in [lo, lo + n)
     while (n > 1) {
       const int gap = (n + 31) / 32;
-      const bool here = lane * gap < n && q.units_before(g, lo + lane * gap) <= at;
+      const bool here = lane * gap < n && Items::units_before(g, q, lo + lane * gap) <= at;
       const int k = 31 - __clz(__ballot_sync(0xffffffffu, here));
       n = min(gap, n - k * gap);
       lo += k * gap;
     }
     if (lane == 0) {
       out[2] = lo;
-      out[3] = static_cast<int>(at - q.units_before(g, lo));
+      out[3] = static_cast<int>(at - Items::units_before(g, q, lo));
     }
   }
   __syncthreads();

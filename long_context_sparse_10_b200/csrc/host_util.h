@@ -18,6 +18,7 @@ int out_proj_device_error(bool clear);
 int cp_merge_device_error(bool clear);
 int gqa_device_error(bool clear);
 int gqa_cache_device_error(bool clear);
+int gqa_mass_device_error(bool clear);
 
 // Records a printf-style message for csa_last_error() and returns `s`.
 csa_status fail(csa_status s, const char* fmt, ...);
