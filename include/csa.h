@@ -606,9 +606,6 @@ CSA_API csa_status gqa_cache_append(const void* k, const void* v, const gqa_cach
 CSA_API csa_status gqa_cache_mass(const void* q, const float* lse, const gqa_cache* cache, const gqa_batch* batch,
                                   int32_t H, float scale, void* stream);
 
-/* Workspace bytes gqa_cache_evict needs. */
-CSA_API size_t gqa_cache_evict_workspace_size(int32_t n_seqs, int32_t H_kv, int32_t max_pages, int32_t page_size);
-
 /*
  * gqa_cache_evict -- cuts caches down to `budget` tokens by accumulated weight.
  * A sequence of L <= budget tokens keeps them all.  Otherwise each kv head on
@@ -625,10 +622,11 @@ CSA_API size_t gqa_cache_evict_workspace_size(int32_t n_seqs, int32_t H_kv, int3
  *         -1 padded;  new_len int32 [n_seqs] (output): min(L, budget), not
  *         the array cache_len
  *   n_sink, n_recent >= 0, n_sink + n_recent <= budget, budget >= 1
+ *   Needs no workspace.
  */
 CSA_API csa_status gqa_cache_evict(const gqa_cache* cache, const gqa_batch* batch, int32_t budget, int32_t n_sink,
                                    int32_t n_recent, const int32_t* new_table, int32_t new_max_pages, int32_t* kept,
-                                   int32_t* new_len, void* workspace, size_t workspace_bytes, void* stream);
+                                   int32_t* new_len, void* stream);
 
 #ifdef __cplusplus
 }

@@ -607,7 +607,7 @@ def gqa_cache_mass(q, lse, cache: GqaCache, batch: GqaBatch, scale, *, stream=No
 
 
 def gqa_cache_evict(cache: GqaCache, batch: GqaBatch, budget, new_table, *, sink=0, recent=0, kept=None, new_len=None,
-                    workspace=None, stream=None):
+                    stream=None):
     """Cuts caches of more than ``budget`` tokens down to it: every kv head keeps its first ``sink`` and last
     ``recent`` tokens and the heaviest (cache.mass) of those between, copied in order to the pages of new_table
     int32 [n_seqs, pages], which no sequence of the call reads.  Returns (kept int32 [n_seqs, H_kv, budget], -1
@@ -624,10 +624,6 @@ def gqa_cache_evict(cache: GqaCache, batch: GqaBatch, budget, new_table, *, sink
             new_len = torch.empty(n, dtype=torch.int32, device=dev)
         kp = _tensor(kept, "kept", torch.int32, (n, cd.n_kv_heads, budget), dev)
         np_ = _tensor(new_len, "new_len", torch.int32, (n,), dev)
-        if workspace is None:
-            need = lib.gqa_cache_evict_workspace_size(n, cd.n_kv_heads, bd.max_pages, cd.page_size)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         _check(lib.gqa_cache_evict(ctypes.byref(cd), ctypes.byref(bd), budget, sink, recent, tp, new_table.shape[1],
-                                   kp, np_, _ptr(workspace), 0 if workspace is None else workspace.numel(), st),
-               "gqa_cache_evict")
+                                   kp, np_, st), "gqa_cache_evict")
     return kept, new_len

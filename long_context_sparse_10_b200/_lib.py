@@ -66,8 +66,7 @@ SIGNATURES = {
     "gqa_dense_paged": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_f32, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "gqa_cache_append": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp]),
     "gqa_cache_mass": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_f32, c_vp]),
-    "gqa_cache_evict_workspace_size": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
-    "gqa_cache_evict": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "gqa_cache_evict": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_vp]),
 }
 
 

@@ -1,5 +1,7 @@
 // The paged cache of the grouped-head (GQA) attention: appending a chunk, and
 // eviction by accumulated weight.
+#include <cooperative_groups.h>
+
 #include "gqa_device.cuh"
 #include "gqa_host.h"
 
@@ -47,11 +49,14 @@ __global__ void __launch_bounds__(256) gqa_append_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// Eviction.  Select: one block per (sequence, kv head); a radix select over
-// the order-preserving 32-bit keys of the middle tokens' mass finds the cut
-// (its key and how many of the tokens equal to it are kept, the first ones),
-// then each warp counts and emits its own contiguous run of positions, so the
-// list comes out ascending.  Gather: the kept tokens' planes to the new pages.
+// Eviction.  Select: a cluster of blocks per (sequence, kv head), each with its
+// run of the positions.  The order-preserving 32-bit keys of the middle tokens'
+// mass are read once, into shared memory where they fit; three radix rounds (11,
+// 11 and 10 bits) over histograms added up across the cluster find the cut: its
+// key, and how many of the tokens equal to it are kept (the first ones).  Each
+// warp then counts and emits its own contiguous run of positions, so the list
+// comes out ascending.  Gather: the kept tokens' planes to the new pages, 16
+// bytes a thread and several loads in flight.
 // ---------------------------------------------------------------------------
 struct EvictParams {
   Pool c;
@@ -62,101 +67,151 @@ struct EvictParams {
   int budget, sink, recent;
   int32_t* kept;
   int32_t* new_len;
+  int held;  // keys a block holds in shared memory
 };
+
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxHeld = 49152;  // keys a block can hold (192 KB)
 
 __device__ __forceinline__ uint32_t mass_key(float m) { return m != m ? 0xffffffffu : f2key(m + 0.f); }
 
-__global__ void __launch_bounds__(1024) gqa_evict_select_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __grid_constant__ EvictParams p) {
   pdl_wait();
-  __shared__ int hist[256];
-  __shared__ int cnt_gt[32], cnt_eq[32];
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ int hist[kBins], total[kBins];
+  __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps], rank_gt, rank_eq;
   __shared__ uint32_t cut[2];
+  extern __shared__ __align__(16) uint32_t keys[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x, s = blockIdx.y;
+  const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int h = blockIdx.y, s = blockIdx.z;
   int32_t* kept = p.kept + (static_cast<int64_t>(s) * p.c.Hkv + h) * p.budget;
   const int32_t* table = p.block_table + static_cast<int64_t>(s) * p.max_pages;
   int L = __ldg(p.cache_len + s);
   L = min(max(L, 0), p.max_pages * p.c.page);
-  if (h == 0 && tid == 0) p.new_len[s] = min(L, p.budget);
-  if (L <= p.budget) {
-    for (int j = tid; j < p.budget; j += 1024) kept[j] = j < L ? j : -1;
+  if (h == 0 && rank == 0 && tid == 0) p.new_len[s] = min(L, p.budget);
+  if (L <= p.budget) {  // every block of the cluster
+    for (int j = rank * kSelThreads + tid; j < p.budget; j += ranks * kSelThreads) kept[j] = j < L ? j : -1;
     return;
   }
   const int lo = p.sink, hi = L - p.recent, want = p.budget - p.sink - p.recent;
+  // this block's positions [a, b); runs of 512 split evenly among the warps
+  const int per = (L + ranks * kSelThreads - 1) / (ranks * kSelThreads) * kSelThreads;
+  const int a = min(rank * per, L), b = min(a + per, L);
+  const bool held = per <= p.held;
   auto key_of = [&](int j) -> uint32_t {
     const int64_t at = slot_of(p.c, table, p.max_pages, h, j);
     return mass_key(at < 0 ? 0.f : p.c.mass[at]);
   };
-  uint32_t prefix = 0, mask = 0;
-  int need = want;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int j = lo + tid; j < hi; j += 1024) {
-      const uint32_t k = key_of(j);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+  if (held) {
+    // four positions lie in one page, on a 16-byte boundary
+    for (int j = a + 4 * tid; j < b; j += 4 * kSelThreads) {
+      const int64_t at = slot_of(p.c, table, p.max_pages, h, j);
+      const float4 m = at < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(p.c.mass + at);
+      *reinterpret_cast<uint4*>(keys + (j - a)) = make_uint4(mass_key(m.x), mass_key(m.y), mass_key(m.z), mass_key(m.w));
     }
-    __syncthreads();
-    if (warp == 0) {
-      // lane l holds bins 255 - 8 l .. 248 - 8 l, from the top
-      int c8 = 0;
-      for (int i = 0; i < 8; ++i) c8 += hist[255 - 8 * lane - i];
-      int inc = c8;
+  }
+  uint32_t prefix = 0;
+  int need = want;  // of the keys that share the prefix
+  if (want > 0) {
+#pragma unroll 1
+    for (int round = 0; round < 3; ++round) {
+      const int shift = round == 0 ? 21 : (round == 1 ? 10 : 0), bits = round == 2 ? 10 : 11;
+      const uint32_t mask = round == 0 ? 0u : ~0u << (round == 1 ? 21 : 10);
+      for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      for (int j = max(a, lo) + tid; j < min(b, hi); j += kSelThreads) {
+        const uint32_t k = held ? keys[j - a] : key_of(j);
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+      }
+      cluster.sync();
+      // the cluster's sums: each block adds up a part of the bins and gives it to all
+      const int part = kBins / ranks;
+      for (int i = rank * part + tid; i < (rank + 1) * part; i += kSelThreads) {
+        int sum = 0;
+        for (int r = 0; r < ranks; ++r) sum += *cluster.map_shared_rank(&hist[i], r);
+        for (int r = 0; r < ranks; ++r) *cluster.map_shared_rank(&total[i], r) = sum;
+      }
+      cluster.sync();
+      // thread t holds bins 2047 - 4 t down to 2044 - 4 t
+      int c4[4], mine = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c4[i] = total[kBins - 1 - 4 * tid - i];
+        mine += c4[i];
+      }
+      int inc = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += v;
       }
-      int before = inc - c8;
-      const bool mine = need > 0 ? (before < need && need <= inc) : lane == 0;
-      if (mine) {
-        int b = 255 - 8 * lane;
-        if (need > 0) {
-          while (before + hist[b] < need) before += hist[b--];
-        }
-        cut[0] = static_cast<uint32_t>(b);
-        cut[1] = static_cast<uint32_t>(need > 0 ? need - before : 0);
+      if (lane == 31) warp_gt[warp] = inc;
+      __syncthreads();
+      int before = inc - mine;
+      for (int w = 0; w < warp; ++w) before += warp_gt[w];
+      if (before < need && need <= before + mine) {
+        int i = 0;
+        while (before + c4[i] < need) before += c4[i++];
+        cut[0] = static_cast<uint32_t>(kBins - 1 - 4 * tid - i);
+        cut[1] = static_cast<uint32_t>(need - before);
       }
+      __syncthreads();
+      prefix |= cut[0] << shift;
+      need = static_cast<int>(cut[1]);
     }
-    __syncthreads();
-    prefix |= cut[0] << shift;
-    mask |= 255u << shift;
-    need = static_cast<int>(cut[1]);
-    __syncthreads();
   }
-  // want == 0: nothing of the middle, whatever its keys are
-  const int seg = ((L + 31) / 32 + 31) / 32 * 32;  // positions per warp
-  const int a = min(warp * seg, L), b = min(a + seg, L);
+  // kept: sink, recent, keys above the cut, and the first `need` keys equal to it
+  const int seg = per / kSelWarps;  // positions per warp, a multiple of 32
+  const int wa = min(a + warp * seg, b), wb = min(wa + seg, b);
   auto classify = [&](int j, bool& gt, bool& eq) {
     gt = eq = false;
-    if (j >= b) return;
+    if (j >= wb) return;
     if (j < lo || j >= hi) {
       gt = true;
     } else if (want > 0) {
-      const uint32_t k = key_of(j);
+      const uint32_t k = held ? keys[j - a] : key_of(j);
       gt = k > prefix;
       eq = k == prefix;
     }
   };
+  __syncthreads();
   int ngt = 0, neq = 0;
-  for (int j = a; j < b; j += 32) {
+  for (int j = wa; j < wb; j += 32) {
     bool gt, eq;
     classify(j + lane, gt, eq);
     ngt += __popc(__ballot_sync(0xffffffffu, gt));
     neq += __popc(__ballot_sync(0xffffffffu, eq));
   }
   if (lane == 0) {
-    cnt_gt[warp] = ngt;
-    cnt_eq[warp] = neq;
+    warp_gt[warp] = ngt;
+    warp_eq[warp] = neq;
   }
   __syncthreads();
+  if (warp == 0) {
+    int g = lane < kSelWarps ? warp_gt[lane] : 0, e = lane < kSelWarps ? warp_eq[lane] : 0;
+    g = warp_sum_i(g);
+    e = warp_sum_i(e);
+    if (lane == 0) {
+      rank_gt = g;
+      rank_eq = e;
+    }
+  }
+  cluster.sync();
   int eq_at = 0, out_at = 0;
+  for (int r = 0; r < rank; ++r) {
+    out_at += *cluster.map_shared_rank(&rank_gt, r);
+    eq_at += *cluster.map_shared_rank(&rank_eq, r);
+  }
   for (int w = 0; w < warp; ++w) {
-    eq_at += cnt_eq[w];
-    out_at += cnt_gt[w];
+    out_at += warp_gt[w];
+    eq_at += warp_eq[w];
   }
   out_at += min(eq_at, need);
-  for (int j = a; j < b; j += 32) {
+  for (int j = wa; j < wb; j += 32) {
     bool gt, eq;
     classify(j + lane, gt, eq);
     const uint32_t below = (1u << lane) - 1u;
@@ -168,27 +223,53 @@ __global__ void __launch_bounds__(1024) gqa_evict_select_kernel(const __grid_con
     eq_at += __popc(me);
     out_at += __popc(mt);
   }
+  cluster.sync();  // no block leaves while another may read its counts
 }
+
+constexpr int kGatherTokens = 32;
 
 __global__ void __launch_bounds__(256) gqa_evict_gather_kernel(const __grid_constant__ EvictParams p) {
   pdl_wait();
-  const int h = blockIdx.y, s = blockIdx.z, lane = threadIdx.x & 31;
-  const int32_t* kept = p.kept + (static_cast<int64_t>(s) * p.c.Hkv + h) * p.budget;
-  for (int u = threadIdx.x >> 5; u < 64; u += 8) {
-    const int j = blockIdx.x * 64 + u;
-    if (j >= p.budget) return;
-    const int from = kept[j];
-    if (from < 0) return;
-    const int64_t src = slot_of(p.c, p.block_table + static_cast<int64_t>(s) * p.max_pages, p.max_pages, h, from);
-    const int64_t dst = slot_of(p.c, p.new_table + static_cast<int64_t>(s) * p.new_max_pages, p.new_max_pages, h, j);
-    if (src < 0 || dst < 0) continue;
-    for (int i = lane; i < p.c.kp + p.c.vp; i += 32) {
-      if (i < p.c.kp)
-        p.c.k[dst * p.c.kp + i] = p.c.k[src * p.c.kp + i];
-      else
-        p.c.v[dst * p.c.vp + i - p.c.kp] = p.c.v[src * p.c.vp + i - p.c.kp];
+  __shared__ int64_t src[kGatherTokens], dst[kGatherTokens];
+  const int h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x;
+  const int j0 = blockIdx.x * kGatherTokens;
+  if (tid < kGatherTokens) {
+    const int j = j0 + tid;
+    const int from = j < p.budget ? p.kept[(static_cast<int64_t>(s) * p.c.Hkv + h) * p.budget + j] : -1;
+    int64_t a = -1, b = -1;
+    if (from >= 0) {
+      a = slot_of(p.c, p.block_table + static_cast<int64_t>(s) * p.max_pages, p.max_pages, h, from);
+      b = slot_of(p.c, p.new_table + static_cast<int64_t>(s) * p.new_max_pages, p.new_max_pages, h, j);
     }
-    if (lane == 0) p.c.mass[dst] = p.c.mass[src];
+    src[tid] = b < 0 ? -1 : a;
+    dst[tid] = b;
+    if (a >= 0 && b >= 0) p.c.mass[b] = p.c.mass[a];
+  }
+  __syncthreads();
+  const int per = p.c.kp + p.c.vp, n = kGatherTokens * per;
+  for (int i0 = tid; i0 < n; i0 += 4 * 256) {
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * 256;
+      if (i < n) {
+        const int t = i / per, x = i - t * per;
+        if (src[t] >= 0) v[u] = x < p.c.kp ? p.c.k[src[t] * p.c.kp + x] : p.c.v[src[t] * p.c.vp + x - p.c.kp];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * 256;
+      if (i < n) {
+        const int t = i / per, x = i - t * per;
+        if (src[t] >= 0) {
+          if (x < p.c.kp)
+            p.c.k[dst[t] * p.c.kp + x] = v[u];
+          else
+            p.c.v[dst[t] * p.c.vp + x - p.c.kp] = v[u];
+        }
+      }
+    }
   }
 }
 
@@ -226,11 +307,9 @@ csa_status gqa_cache_append(const void* k, const void* v, const gqa_cache* cache
   return check_launch(what, e);
 }
 
-size_t gqa_cache_evict_workspace_size(int32_t, int32_t, int32_t, int32_t) { return 0; }
-
 csa_status gqa_cache_evict(const gqa_cache* cache, const gqa_batch* batch, int32_t budget, int32_t n_sink,
                            int32_t n_recent, const int32_t* new_table, int32_t new_max_pages, int32_t* kept,
-                           int32_t* new_len, void* workspace, size_t workspace_bytes, void* stream) {
+                           int32_t* new_len, void* stream) {
   using namespace csa;
   const char* what = "gqa_cache_evict";
   clear_error();
@@ -250,8 +329,6 @@ csa_status gqa_cache_evict(const gqa_cache* cache, const gqa_batch* batch, int32
   CSA_REQUIRE(new_table != batch->block_table, "%s: the new table is the old one: eviction needs pages of its own", what);
   CSA_REQUIRE(new_len != batch->cache_len, "%s: new_len is cache_len: it needs an array of its own", what);
   CSA_REQUIRE(batch->n_seqs <= 65535, "%s: at most 65535 sequences", what);
-  (void)workspace;
-  (void)workspace_bytes;
   EvictParams p;
   p.c = pool_of(cache);
   p.block_table = batch->block_table;
@@ -267,10 +344,23 @@ csa_status gqa_cache_evict(const gqa_cache* cache, const gqa_batch* batch, int32
   p.new_len = new_len;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   prof_begin(s);
-  cudaError_t e = launch_pdl(gqa_evict_select_kernel, dim3(cache->n_kv_heads, batch->n_seqs), dim3(1024), 0, s, 1, p);
+  // A cluster per list: enough blocks that each has about 4096 positions of the longest (at 65536 positions and 32
+  // lists: 274 us with one block of 1024 threads per list).
+  const int longest = batch->max_pages * cache->page_size;
+  int ranks = 1;
+  while (ranks < kMaxCluster && longest > 4096 * ranks) ranks *= 2;
+  p.held = (longest + ranks * kSelThreads - 1) / (ranks * kSelThreads) * kSelThreads;
+  if (p.held > kMaxHeld) p.held = 0;  // read again each time
+  const int smem = p.held * 4;
+  if (!ensure_smem(reinterpret_cast<const void*>(gqa_evict_select_kernel), smem))
+    return fail(CSA_ERR_CUDA, "%s: cannot raise the shared memory limit", what);
+  prof_begin(s);
+  cudaError_t e = launch_pdl(gqa_evict_select_kernel, dim3(ranks, cache->n_kv_heads, batch->n_seqs), dim3(kSelThreads),
+                             static_cast<size_t>(smem), s, ranks, p);
   prof_end(s);
   if (csa_status st = check_launch(what, e); st != CSA_OK) return st;
-  e = launch_pdl(gqa_evict_gather_kernel, dim3((budget + 63) / 64, cache->n_kv_heads, batch->n_seqs), dim3(256), 0, s,
+  e = launch_pdl(gqa_evict_gather_kernel,
+                 dim3((budget + kGatherTokens - 1) / kGatherTokens, cache->n_kv_heads, batch->n_seqs), dim3(256), 0, s,
                  1, p);
   return check_launch(what, e);
 }

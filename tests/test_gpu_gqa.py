@@ -107,11 +107,11 @@ def test_a_prompt_batch_gives_the_same_bits_every_time(dims):
 class Case:
     """A paged cache with its pages in random order; what no token lies in holds NaN."""
 
-    def __init__(self, seed, lens, n, Hkv, G, dims, page, extra_rows=0, junk=float("nan"), std=1.0):
+    def __init__(self, seed, lens, n, Hkv, G, dims, page, extra_rows=0, junk=float("nan"), std=1.0, width=None):
         g = np.random.default_rng(seed)
         self.g, self.lens, self.n, self.Hkv, self.G, self.dims, self.page = g, lens, n, Hkv, G, dims, page
         need = [-(-max(L, 0) // page) for L in lens]
-        width = max(max(need), 1) + 1
+        width = width or max(max(need), 1) + 1
         P = sum(need) + 2
         order = list(g.permutation(P))
         self.table = np.full((len(lens), width), -5, np.int32)
@@ -365,17 +365,19 @@ def test_accumulated_weight(lens, n, Hkv, G, dims, page):
     assert np.all(np.abs(got - want) <= tol), float((np.abs(got - want) - tol).max())
 
 
-@pytest.mark.parametrize("lens,Hkv,dims,page,budget,sink,recent", [
-    ([300, 64, 65, 0, 1], 2, (128, 128), 16, 64, 4, 16),
-    ([500], 3, (192, 128), 128, 1, 0, 0),
-    ([500, 77], 1, (64, 64), 32, 76, 0, 76),
-    ([500, 77], 1, (64, 64), 32, 76, 76, 0),
-    ([2100, 1030], 2, (64, 64), 64, 1029, 3, 100),
-    ([40, 50], 2, (128, 128), 16, 200, 1, 1),
+@pytest.mark.parametrize("lens,Hkv,dims,page,budget,sink,recent,width", [
+    ([300, 64, 65, 0, 1], 2, (128, 128), 16, 64, 4, 16, None),
+    ([500], 3, (192, 128), 128, 1, 0, 0, None),
+    ([500, 77], 1, (64, 64), 32, 76, 0, 76, None),
+    ([500, 77], 1, (64, 64), 32, 76, 76, 0, None),
+    ([2100, 1030], 2, (64, 64), 64, 1029, 3, 100, None),
+    ([40, 50], 2, (128, 128), 16, 200, 1, 1, None),
+    ([9000, 30011, 4097], 1, (64, 64), 64, 3000, 4, 64, None),   # several blocks per list
+    ([1500, 700, 3000], 2, (64, 64), 16, 640, 0, 1, 25000),      # a table too wide for keys to be held on chip
 ])
 @pytest.mark.parametrize("kind", ["random", "equal", "few"])
-def test_evict(lens, Hkv, dims, page, budget, sink, recent, kind):
-    c = Case(sum(lens) + budget, lens, [0] * len(lens), Hkv, 1, dims, page)
+def test_evict(lens, Hkv, dims, page, budget, sink, recent, width, kind):
+    c = Case(sum(lens) + budget, lens, [0] * len(lens), Hkv, 1, dims, page, width=width)
     pages = -(-budget // page)
     P = c.k.shape[0]
     new = P + c.g.permutation(len(lens) * pages).reshape(len(lens), pages)

@@ -130,7 +130,7 @@ def test_calls_without_rows_are_no_ops(lib):
     assert prompt(lib, p=packed(total_tokens=0, max_tokens=0)) == OK
     assert lib.gqa_cache_append(16, 16, ref(cache()), ref(batch(total_q=0)), None) == OK
     assert lib.gqa_cache_mass(16, 16, ref(cache()), ref(batch(n_seqs=0)), 8, 0.1, None) == OK
-    assert lib.gqa_cache_evict(ref(cache()), ref(batch(n_seqs=0)), 16, 0, 0, 32, 1, 16, 32, None, 0, None) == OK
+    assert lib.gqa_cache_evict(ref(cache()), ref(batch(n_seqs=0)), 16, 0, 0, 32, 1, 16, 32, None) == OK
 
 
 def test_append_and_mass_refusals(lib):
@@ -159,7 +159,7 @@ def test_evict_refusals(lib, kw, word):
     a = dict(c=cache(), b=batch(), budget=16, sink=0, recent=0, table=32, width=1, kept=16, new_len=32)
     a.update(kw)
     st = lib.gqa_cache_evict(ref(a["c"]), ref(a["b"]), a["budget"], a["sink"], a["recent"], a["table"], a["width"],
-                             a["kept"], a["new_len"], None, 0, None)
+                             a["kept"], a["new_len"], None)
     assert st == INV and word in lib.csa_last_error(), lib.csa_last_error()
 
 
