@@ -454,39 +454,42 @@ def hca_dense_mqa_packed(q, packed: Packed, cache: KVCache, m_prime, win_k, win_
 
 
 def _tensor(t, name, dtype, shape, device):
-    """A contiguous CUDA tensor of this type, shape (None: any size) and device; its address."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return _ptr(t)
+    """The address of a contiguous CUDA tensor of this type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-class _On:
-    """The device of a call's tensors, and the stream it runs on, as the current ones (outputs and scratch
-    are then allocated for that stream)."""
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("tensor must live on a CUDA device")
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+def _elsewhere(device, stream):
+    """None where a call runs on the current device and stream, else a context that makes its own the current ones
+    (outputs and scratch are then allocated for that stream)."""
+    if device.type != "cuda":
+        raise ValueError("tensor must live on a CUDA device")
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
-        self.cm = None
-        if stream is not None:
-            self.cm = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.cm = torch.cuda.device(device)
+        return torch.cuda.stream(stream)
+    return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.cm is not None:
-            self.cm.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
-    def __exit__(self, *exc):
-        if self.cm is not None:
-            self.cm.__exit__(*exc)
+# torch's own short way to the current stream's handle, where it has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream(device):
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _dims(t, n, name):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
 
 
 @dataclasses.dataclass
@@ -497,14 +500,14 @@ class GqaCache:
     v: torch.Tensor
     mass: torch.Tensor | None = None
 
-    def desc(self) -> _lib.GqaCacheDesc:
-        dev = self.k.device
-        P, H, S, d = self.k.shape
-        return _lib.GqaCacheDesc(_tensor(self.k, "cache.k", torch.bfloat16, (P, H, S, d), dev),
-                                 _tensor(self.v, "cache.v", torch.bfloat16, (P, H, S, None), dev),
-                                 None if self.mass is None else
-                                 _tensor(self.mass, "cache.mass", torch.float32, (P, H, S), dev),
-                                 P, S, H, d, self.v.shape[3])
+    def desc(self, device) -> _lib.GqaCacheDesc:
+        k, v, mass = self.k, self.v, self.mass
+        P, H, S, d = _dims(k, 4, "cache.k")
+        dv = _dims(v, 4, "cache.v")[3]
+        return _lib.GqaCacheDesc(_tensor(k, "cache.k", torch.bfloat16, (P, H, S, d), device),
+                                 _tensor(v, "cache.v", torch.bfloat16, (P, H, S, dv), device),
+                                 None if mass is None else _tensor(mass, "cache.mass", torch.float32, (P, H, S), device),
+                                 P, S, H, d, dv)
 
 
 @dataclasses.dataclass
@@ -520,7 +523,7 @@ class GqaBatch:
     total_q: int = 0
 
     def desc(self, device) -> _lib.GqaBatchDesc:
-        n, m = self.block_table.shape
+        n, m = _dims(self.block_table, 2, "block_table")
         return _lib.GqaBatchDesc(_tensor(self.block_table, "block_table", torch.int32, (n, m), device),
                                  _tensor(self.cache_len, "cache_len", torch.int32, (n,), device),
                                  None if self.cu_q is None else
@@ -532,77 +535,85 @@ def gqa_dense_workspace_size(max_q, H, H_kv, d_v) -> int:
     return int(_lib.load().gqa_dense_workspace_size(max_q, H, H_kv, d_v))
 
 
-def _gqa_buffers(q, d_v, max_q, H_kv, out, lse, workspace):
+def _gqa_buffers(lib, q, d_v, max_q, H_kv, out, lse, workspace):
     R, H, _ = q.shape
     dev = q.device
     if out is None:
-        out = torch.empty(R, H, d_v, dtype=torch.bfloat16, device=dev)
+        out = torch.empty((R, H, d_v), dtype=torch.bfloat16, device=dev)
     if lse is None:
-        lse = torch.empty(R, H, dtype=torch.float32, device=dev)
+        lse = torch.empty((R, H), dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty(gqa_dense_workspace_size(max_q, H, H_kv, d_v), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(lib.gqa_dense_workspace_size(max_q, H, H_kv, d_v), dtype=torch.uint8, device=dev)
     return (out, lse, workspace, _tensor(out, "out", torch.bfloat16, (R, H, d_v), dev),
-            _tensor(lse, "lse", torch.float32, (R, H), dev), _ptr(workspace))
+            _tensor(lse, "lse", torch.float32, (R, H), dev),
+            _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), dev))
 
 
 def gqa_dense_packed(q, k, v, packed: Packed, scale, *, out=None, lse=None, workspace=None, stream=None):
     """Causal attention over whole packed prompts with grouped heads: row t of a sequence sees its tokens 0 .. t,
     query head h reads kv head h // (H / H_kv).  Returns (out, lse)."""
-    lib = _lib.load()
     dev = q.device
-    R, H, d_qk = q.shape
-    H_kv, d_v = v.shape[1], v.shape[2]
-    with _On(dev, stream) as st:
-        qp = _tensor(q, "q", torch.bfloat16, (packed.total_tokens, H, d_qk), dev)
-        kp = _tensor(k, "k", torch.bfloat16, (R, H_kv, d_qk), dev)
-        vp = _tensor(v, "v", torch.bfloat16, (R, H_kv, d_v), dev)
-        out, lse, workspace, op, lp, wp = _gqa_buffers(q, d_v, packed.max_tokens, H_kv, out, lse, workspace)
-        pd = packed.desc()
-        _check(lib.gqa_dense_packed(qp, kp, vp, ctypes.byref(pd), H, H_kv, d_qk, d_v, scale, op, lp, wp,
-                                    workspace.numel(), st), "gqa_dense_packed")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return gqa_dense_packed(q, k, v, packed, scale, out=out, lse=lse, workspace=workspace)
+    lib = _lib.load()
+    R, H, d_qk = _dims(q, 3, "q")
+    _, H_kv, d_v = _dims(v, 3, "v")
+    qp = _tensor(q, "q", torch.bfloat16, (packed.total_tokens, H, d_qk), dev)
+    kp = _tensor(k, "k", torch.bfloat16, (R, H_kv, d_qk), dev)
+    vp = _tensor(v, "v", torch.bfloat16, (R, H_kv, d_v), dev)
+    if packed.cu_tokens.device != dev:
+        raise ValueError(f"the packed offsets are on {packed.cu_tokens.device}, not on {dev}")
+    out, lse, workspace, op, lp, wp = _gqa_buffers(lib, q, d_v, packed.max_tokens, H_kv, out, lse, workspace)
+    _check(lib.gqa_dense_packed(qp, kp, vp, ctypes.byref(packed.desc()), H, H_kv, d_qk, d_v, scale, op, lp, wp,
+                                workspace.numel(), _current_stream(dev)), "gqa_dense_packed")
     return out, lse
 
 
 def gqa_dense_paged(q, cache: GqaCache, batch: GqaBatch, scale, *, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of a chunk of new tokens (one: decode) over the paged cache that holds them already.
     Returns (out, lse)."""
-    lib = _lib.load()
     dev = q.device
-    H, d_qk = q.shape[1], q.shape[2]
-    with _On(dev, stream) as st:
-        cd, bd = cache.desc(), batch.desc(dev)
-        if cache.k.device != dev:
-            raise ValueError(f"the cache is on {cache.k.device}, not on {dev}")
-        qp = _tensor(q, "q", torch.bfloat16, (batch.total_q, H, cd.d_qk), dev)
-        out, lse, workspace, op, lp, wp = _gqa_buffers(q, cd.d_v, batch.max_q, cd.n_kv_heads, out, lse, workspace)
-        _check(lib.gqa_dense_paged(qp, ctypes.byref(cd), ctypes.byref(bd), H, scale, op, lp, wp, workspace.numel(),
-                                   st), "gqa_dense_paged")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return gqa_dense_paged(q, cache, batch, scale, out=out, lse=lse, workspace=workspace)
+    lib = _lib.load()
+    cd, bd = cache.desc(dev), batch.desc(dev)
+    qp = _tensor(q, "q", torch.bfloat16, (batch.total_q, _dims(q, 3, "q")[1], cd.d_qk), dev)
+    out, lse, workspace, op, lp, wp = _gqa_buffers(lib, q, cd.d_v, batch.max_q, cd.n_kv_heads, out, lse, workspace)
+    _check(lib.gqa_dense_paged(qp, ctypes.byref(cd), ctypes.byref(bd), q.shape[1], scale, op, lp, wp,
+                               workspace.numel(), _current_stream(dev)), "gqa_dense_paged")
     return out, lse
 
 
 def gqa_cache_append(k, v, cache: GqaCache, batch: GqaBatch, *, stream=None):
     """Writes the new tokens' k bf16 [total_q, H_kv, d_qk] and v bf16 [total_q, H_kv, d_v] into their slots, and 0
     into the slots' mass where the cache has one."""
-    lib = _lib.load()
     dev = cache.k.device
-    with _On(dev, stream) as st:
-        cd, bd = cache.desc(), batch.desc(dev)
-        kp = _tensor(k, "k", torch.bfloat16, (batch.total_q, cd.n_kv_heads, cd.d_qk), dev)
-        vp = _tensor(v, "v", torch.bfloat16, (batch.total_q, cd.n_kv_heads, cd.d_v), dev)
-        _check(lib.gqa_cache_append(kp, vp, ctypes.byref(cd), ctypes.byref(bd), st), "gqa_cache_append")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return gqa_cache_append(k, v, cache, batch)
+    lib = _lib.load()
+    cd, bd = cache.desc(dev), batch.desc(dev)
+    kp = _tensor(k, "k", torch.bfloat16, (batch.total_q, cd.n_kv_heads, cd.d_qk), dev)
+    vp = _tensor(v, "v", torch.bfloat16, (batch.total_q, cd.n_kv_heads, cd.d_v), dev)
+    _check(lib.gqa_cache_append(kp, vp, ctypes.byref(cd), ctypes.byref(bd), _current_stream(dev)), "gqa_cache_append")
 
 
 def gqa_cache_mass(q, lse, cache: GqaCache, batch: GqaBatch, scale, *, stream=None):
     """Adds to cache.mass the attention weight the chunk's rows give every cached token, summed over the rows and
     the heads of a group; lse is gqa_dense_paged's of the same rows.  Returns cache.mass."""
-    lib = _lib.load()
     dev = cache.k.device
-    H = q.shape[1]
-    with _On(dev, stream) as st:
-        cd, bd = cache.desc(), batch.desc(dev)
-        qp = _tensor(q, "q", torch.bfloat16, (batch.total_q, H, cd.d_qk), dev)
-        lp = _tensor(lse, "lse", torch.float32, (batch.total_q, H), dev)
-        _check(lib.gqa_cache_mass(qp, lp, ctypes.byref(cd), ctypes.byref(bd), H, scale, st), "gqa_cache_mass")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return gqa_cache_mass(q, lse, cache, batch, scale)
+    lib = _lib.load()
+    cd, bd = cache.desc(dev), batch.desc(dev)
+    H = _dims(q, 3, "q")[1]
+    qp = _tensor(q, "q", torch.bfloat16, (batch.total_q, H, cd.d_qk), dev)
+    lp = _tensor(lse, "lse", torch.float32, (batch.total_q, H), dev)
+    _check(lib.gqa_cache_mass(qp, lp, ctypes.byref(cd), ctypes.byref(bd), H, scale, _current_stream(dev)),
+           "gqa_cache_mass")
     return cache.mass
 
 
@@ -612,18 +623,21 @@ def gqa_cache_evict(cache: GqaCache, batch: GqaBatch, budget, new_table, *, sink
     ``recent`` tokens and the heaviest (cache.mass) of those between, copied in order to the pages of new_table
     int32 [n_seqs, pages], which no sequence of the call reads.  Returns (kept int32 [n_seqs, H_kv, budget], -1
     padded, and new_len int32 [n_seqs])."""
-    lib = _lib.load()
     dev = cache.k.device
-    n = batch.block_table.shape[0]
-    with _On(dev, stream) as st:
-        cd, bd = cache.desc(), batch.desc(dev)
-        tp = _tensor(new_table, "new_table", torch.int32, (n, None), dev)
-        if kept is None:
-            kept = torch.empty(n, cd.n_kv_heads, budget, dtype=torch.int32, device=dev)
-        if new_len is None:
-            new_len = torch.empty(n, dtype=torch.int32, device=dev)
-        kp = _tensor(kept, "kept", torch.int32, (n, cd.n_kv_heads, budget), dev)
-        np_ = _tensor(new_len, "new_len", torch.int32, (n,), dev)
-        _check(lib.gqa_cache_evict(ctypes.byref(cd), ctypes.byref(bd), budget, sink, recent, tp, new_table.shape[1],
-                                   kp, np_, st), "gqa_cache_evict")
+    if (ctx := _elsewhere(dev, stream)) is not None:
+        with ctx:
+            return gqa_cache_evict(cache, batch, budget, new_table, sink=sink, recent=recent, kept=kept,
+                                   new_len=new_len)
+    lib = _lib.load()
+    cd, bd = cache.desc(dev), batch.desc(dev)
+    n, H, pages = bd.n_seqs, cd.n_kv_heads, _dims(new_table, 2, "new_table")[1]
+    tp = _tensor(new_table, "new_table", torch.int32, (n, pages), dev)
+    if kept is None:
+        kept = torch.empty((n, H, max(budget, 0)), dtype=torch.int32, device=dev)
+    if new_len is None:
+        new_len = torch.empty((n,), dtype=torch.int32, device=dev)
+    kp = _tensor(kept, "kept", torch.int32, (n, H, budget), dev)
+    np_ = _tensor(new_len, "new_len", torch.int32, (n,), dev)
+    _check(lib.gqa_cache_evict(ctypes.byref(cd), ctypes.byref(bd), budget, sink, recent, tp, pages, kp, np_,
+                               _current_stream(dev)), "gqa_cache_evict")
     return kept, new_len
