@@ -175,6 +175,19 @@ __device__ __forceinline__ float probabilities(float* v, float a, float b, uint3
   return (l0 + l1) + (l2 + l3);
 }
 
+// The tensor core's turn: an MMA warp says that it issues a stream's last product of a tile and its next scores, and the
+// other lets them pass first, so that the core runs one stream's after the other's instead of alternating between them.
+// (Alternating, both streams got their scores at the same, later time, and then kept the core idle together.)  Nothing
+// but the order depends on it: a warp that reads the word too early does no harm, and waiting ends by itself.
+__device__ __forceinline__ void await_turn(const uint32_t* busy) {
+  uint32_t other = 1;
+  for (int it = 0; it < 64 && other; ++it)
+    asm volatile("ld.volatile.shared::cta.u32 %0, [%1];\n" : "=r"(other) : "r"(smem_u32(busy)) : "memory");
+}
+__device__ __forceinline__ void set_turn(uint32_t* busy, uint32_t v) {
+  asm volatile("st.volatile.shared::cta.u32 [%0], %1;\n" ::"r"(smem_u32(busy)), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
 }
@@ -233,11 +246,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* vland = oempty + 2;            // [2] V of a stream's tile with keys past the end has arrived
   int64_t* scratch = reinterpret_cast<int64_t*>(vland + 2);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(scratch + 40);
+  uint32_t* busy = tslot + 1;  // [2] a stream's MMAs are being issued
   float2* stat = reinterpret_cast<float2*>(smem + ((S::kStatOff + 15) / 16) * 16);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Geometry& g = p.g;
 
   if (tid == 0) {
+    busy[0] = busy[1] = 0;
     for (int i = 0; i < S::kKStages; ++i) {
       tc::bar_init(&kfull[i], 1);
       tc::bar_init(&kempty[i], 2);
@@ -361,65 +376,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       healthy = s == 0 || one ? wait_warp(&qfull[0], items & 1) : wait_warp(&qfull[1], pairs & 1);
       pairs += one ? 0 : 1;
       const uint64_t qd = q_desc + (one ? 0 : __shfl_sync(0xffffffffu, s * (S::kQBytes >> 4), 0));
-      // The stream's scores of tile j, and word that it is done with the tile as K (with the last one, with the
-      // queries too).  Every tile's word comes from both streams, after the tile has arrived.
-      auto scores = [&](int j) {
-        const int t = base + j - t0, st = t % S::kKStages;
-        if (!wait_warp(&kfull[st], (t / S::kKStages) & 1)) return false;
-        const bool mine = steps_of(one, s, j, ks) > 0;
-        const uint64_t b = k_desc + __shfl_sync(0xffffffffu, st * (S::kQBytes >> 4), 0);
+      const int ahead = one ? 2 : 1;  // tiles to the stream's next
+      bool fresh = true;  // no product yet
+      // Every tile's stages are given back by both streams, each after the tile has arrived (and, where it uses it, when
+      // its products are complete); with the last K tile, the queries too.
+      // First the stream's first scores (its own of tile t0, or of t0 and t0 + 1), then tile by tile the products of
+      // tile j, the last one followed at once by the scores of the stream's next tile jn.
+      for (int j = t0 - ahead; j < t1 && healthy; ++j) {
+        const int jn = j + ahead;
+        const int t = base + j - t0, tn = t + ahead;
+        const int sv = j >= t0 ? t % S::kVStages : 0, sk = tn % S::kKStages;
+        const int c = j >= t0 ? steps_of(one, s, j, ks) : 0;
+        const bool next = jn < t1, mine = next && steps_of(one, s, jn, ks) > 0;
+        const uint64_t kd = k_desc + __shfl_sync(0xffffffffu, sk * (S::kQBytes >> 4), 0);
+        const uint64_t vd = v_desc + __shfl_sync(0xffffffffu, sv * (S::kVBytes >> 4), 0);
+        if (j >= t0) healthy = wait_warp(&vfull[sv], (t / S::kVStages) & 1);
+        bar_arrive_if(&vland[s], lane == 0 && c > 0 && clears_tail(one, s, j, ks0, w.q.L));
+        if (c > 0 && fresh && items > 0) healthy = healthy && wait_warp(&oempty[s], (items - 1) & 1);
+        if (c == 2) {
+          healthy = healthy && wait_warp(&pfull[2 * s], parity & 1u);
+          parity ^= 1u;
+          tc::fence_after_sync();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kStep / 16; ++k)
+              mma_bf16_ts(tO, tS + k * 8, vd + k * (2048 >> 4), id_pv, k == 0 ? (fresh ? 0u : 1u) : 1u);
+          }
+          __syncwarp();
+          fresh = false;
+        }
+        if (next) healthy = healthy && wait_warp(&kfull[sk], (tn / S::kKStages) & 1);
+        if (c > 0) healthy = healthy && wait_warp(&pfull[2 * s + c - 1], (parity >> (c - 1)) & 1u);
+        if (!healthy) break;
+        if (c > 0) parity ^= 1u << (c - 1);
+        const uint64_t vh = vd + (c == 2 ? kStep * 128 >> 4 : 0);
+        const uint32_t tP = tS + (c == 2 ? kStep / 2 : 0), add = fresh ? 0u : 1u;
+        if (c > 0) await_turn(&busy[s ^ 1]);
         tc::fence_after_sync();
         if (elect_one()) {
+          set_turn(&busy[s], 1);
+          if (c > 0) {
+#pragma unroll
+            for (int k = 0; k < kStep / 16; ++k) mma_bf16_ts(tO, tP + k * 8, vh + k * (2048 >> 4), id_pv, k == 0 ? add : 1u);
+          }
           if (mine) {
 #pragma unroll
             for (int k = 0; k < DQK / 16; ++k) {
               const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;  // descriptors count 16-byte units
-              tc::mma_bf16_ss(tS, qd + o, b + o, id_qk, k != 0 ? 1u : 0u);
+              tc::mma_bf16_ss(tS, qd + o, kd + o, id_qk, k != 0 ? 1u : 0u);
             }
             tc::mma_commit(&sfull[s]);
           }
-          tc::mma_commit(&kempty[st]);
-          if (j == t1 - 1) {
+          set_turn(&busy[s], 0);
+          if (c > 0) tc::mma_commit(&odone[s]);
+          if (j >= t0) tc::mma_commit(&vempty[sv]);
+          if (next) tc::mma_commit(&kempty[sk]);
+          if (jn == t1 - 1) {
             tc::mma_commit(&qempty[0]);
             tc::mma_commit(&qempty[1]);
           }
         }
         __syncwarp();
-        return true;
-      };
-      bool fresh = true;  // no product yet
-      const int ahead = one ? 2 : 1;
-      // Tile by tile the products, each followed by the stream's next scores (those of its first tile come first).
-      for (int j = t0 - ahead; j < t1 && healthy; ++j) {
-        const int jn = j + ahead;
-        if (j >= t0) {
-          const int t = base + j - t0, sv = t % S::kVStages, c = steps_of(one, s, j, ks);
-          healthy = wait_warp(&vfull[sv], (t / S::kVStages) & 1);
-          bar_arrive_if(&vland[s], lane == 0 && c > 0 && clears_tail(one, s, j, ks0, w.q.L));
-          if (c > 0 && fresh && items > 0) healthy = healthy && wait_warp(&oempty[s], (items - 1) & 1);
-          const uint64_t vd = v_desc + __shfl_sync(0xffffffffu, sv * (S::kVBytes >> 4), 0);
-#pragma unroll 1
-          for (int hh = 0; hh < c && healthy; ++hh) {
-            const uint64_t b = vd + hh * (kStep * 128 >> 4);
-            const uint32_t tP = tS + hh * (kStep / 2), add = fresh ? 0u : 1u;
-            healthy = wait_warp(&pfull[2 * s + hh], (parity >> hh) & 1u);
-            if (!healthy) break;
-            tc::fence_after_sync();
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < kStep / 16; ++k) mma_bf16_ts(tO, tP + k * 8, b + k * (2048 >> 4), id_pv, k == 0 ? add : 1u);
-              if (hh + 1 == c) tc::mma_commit(&odone[s]);
-            }
-            __syncwarp();
-            fresh = false;
-            parity ^= 1u << hh;
-          }
-          if (healthy && jn < t1) healthy = scores(jn);
-          if (elect_one()) tc::mma_commit(&vempty[sv]);
-          __syncwarp();
-        } else if (jn < t1) {
-          healthy = scores(jn);
-        }
+        if (c > 0) fresh = false;
       }
       // a stream without a tile here: its previous item's read-out is awaited all the same, so that no phase of
       // oempty is left two behind
