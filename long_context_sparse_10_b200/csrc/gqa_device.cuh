@@ -60,6 +60,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// The same, kept in the source's order.
+__device__ __forceinline__ float exp2_in_order(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Two fp32 operations in one instruction (each rounded as its scalar form).
 __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
   asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %4};\nmov.b64 c, {%5, %5};\n"
