@@ -107,11 +107,25 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
     return mass_key(at < 0 ? 0.f : p.c.mass[at]);
   };
   if (held) {
-    // four positions lie in one page, on a 16-byte boundary
-    for (int j = a + 4 * tid; j < b; j += 4 * kSelThreads) {
-      const int64_t at = slot_of(p.c, table, p.max_pages, h, j);
-      const float4 m = at < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(p.c.mass + at);
-      *reinterpret_cast<uint4*>(keys + (j - a)) = make_uint4(mass_key(m.x), mass_key(m.y), mass_key(m.z), mass_key(m.w));
+    // four positions lie in one page, on a 16-byte boundary; four such loads in flight
+    for (int j0 = a + 4 * tid; j0 < b; j0 += 16 * kSelThreads) {
+      int64_t at[4];
+      float4 m[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + 4 * u * kSelThreads;
+        at[u] = j < b ? slot_of(p.c, table, p.max_pages, h, j) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        m[u] = at[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(p.c.mass + at[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int j = j0 + 4 * u * kSelThreads;
+        if (j < b)
+          *reinterpret_cast<uint4*>(keys + (j - a)) =
+              make_uint4(mass_key(m[u].x), mass_key(m[u].y), mass_key(m[u].z), mass_key(m[u].w));
+      }
     }
   }
   uint32_t prefix = 0;
@@ -131,9 +145,14 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
       // the cluster's sums: each block adds up a part of the bins and gives it to all
       const int part = kBins / ranks;
       for (int i = rank * part + tid; i < (rank + 1) * part; i += kSelThreads) {
-        int sum = 0;
-        for (int r = 0; r < ranks; ++r) sum += *cluster.map_shared_rank(&hist[i], r);
-        for (int r = 0; r < ranks; ++r) *cluster.map_shared_rank(&total[i], r) = sum;
+        int c[kMaxCluster], sum = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) c[r] = r < ranks ? *cluster.map_shared_rank(&hist[i], r) : 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) sum += c[r];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < ranks) *cluster.map_shared_rank(&total[i], r) = sum;
       }
       cluster.sync();
       // thread t holds bins 2047 - 4 t down to 2044 - 4 t
@@ -226,7 +245,7 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
   cluster.sync();  // no block leaves while another may read its counts
 }
 
-constexpr int kGatherTokens = 32;
+constexpr int kGatherTokens = 64;
 
 __global__ void __launch_bounds__(256) gqa_evict_gather_kernel(const __grid_constant__ EvictParams p) {
   pdl_wait();
