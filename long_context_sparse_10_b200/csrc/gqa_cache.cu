@@ -260,9 +260,9 @@ __global__ void __launch_bounds__(256) gqa_evict_gather_kernel(const __grid_cons
       a = slot_of(p.c, p.block_table + static_cast<int64_t>(s) * p.max_pages, p.max_pages, h, from);
       b = slot_of(p.c, p.new_table + static_cast<int64_t>(s) * p.new_max_pages, p.new_max_pages, h, j);
     }
-    src[tid] = b < 0 ? -1 : a;
+    src[tid] = a;  // -1: a page outside the pool, read as zeros
     dst[tid] = b;
-    if (a >= 0 && b >= 0) p.c.mass[b] = p.c.mass[a];
+    if (b >= 0) p.c.mass[b] = a < 0 ? 0.f : p.c.mass[a];
   }
   __syncthreads();
   const int per = p.c.kp + p.c.vp, n = kGatherTokens * per;
@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(256) gqa_evict_gather_kernel(const __grid_cons
       const int i = i0 + u * 256;
       if (i < n) {
         const int t = i / per, x = i - t * per;
+        v[u] = make_uint4(0, 0, 0, 0);
         if (src[t] >= 0) v[u] = x < p.c.kp ? p.c.k[src[t] * p.c.kp + x] : p.c.v[src[t] * p.c.vp + x - p.c.kp];
       }
     }
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(256) gqa_evict_gather_kernel(const __grid_cons
       const int i = i0 + u * 256;
       if (i < n) {
         const int t = i / per, x = i - t * per;
-        if (src[t] >= 0) {
+        if (dst[t] >= 0) {
           if (x < p.c.kp)
             p.c.k[dst[t] * p.c.kp + x] = v[u];
           else

@@ -284,6 +284,153 @@ def test_replayed_with_other_lengths():
         c.check(out, lse, f"lengths {lens}")
 
 
+def test_a_captured_chunk_replayed_with_other_chunks():
+    # captured for chunks of up to 70 tokens; the same graph then takes one token a sequence, none, and long ones
+    c = Case(35, [500, 300, 90], [70, 1, 30], 2, 4, (192, 128), 32)
+    rows = 101
+    q = c.q.to(DEV)
+    out = torch.empty(rows, 8, 128, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(rows, 8, device=DEV)
+    ws = torch.empty(csa.gqa_dense_workspace_size(70, 8, 2, 128), dtype=torch.uint8, device=DEV)
+    csa.gqa_dense_paged(q, c.cache, c.batch, c.scale, out=out, lse=lse, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        csa.gqa_dense_paged(q, c.cache, c.batch, c.scale, out=out, lse=lse, workspace=ws)
+    for lens, n in (([500, 300, 90], [70, 1, 30]), ([129, 1, 64], [1, 1, 1]), ([400, 300, 70], [0, 31, 70])):
+        c.lens, c.n = lens, n
+        c.cu = [0, n[0], n[0] + n[1], sum(n)]
+        c.batch.cache_len.copy_(i32(lens))
+        c.batch.cu_q.copy_(i32(c.cu))
+        out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        no_device_error()
+        c.check(out, lse, f"chunks {n}")
+        assert torch.all(out[sum(n):] == 5.0)
+
+
+def test_a_captured_decode_step_and_eviction():
+    """append, attention, weight and eviction in one graph; what it computes is what the calls compute one by one."""
+    c = Case(36, [300, 45], [1, 1], 2, 4, (128, 128), 16)
+    pages = 3
+    P = c.k.shape[0]
+    new = i32(P + np.arange(2 * pages).reshape(2, pages))
+    k, v = bf16(c.g, 2, 2, 128).to(DEV), bf16(c.g, 2, 2, 128).to(DEV)
+    q = c.q.to(DEV)
+
+    def pool():
+        pad = [torch.zeros(2 * pages, *t.shape[1:], dtype=t.dtype) for t in (c.k, c.v, c.mass)]
+        return csa.GqaCache(*[torch.cat([t, z]).to(DEV) for t, z in zip((c.k, c.v, c.mass), pad)])
+
+    def step(cache):
+        csa.gqa_cache_append(k, v, cache, c.batch)
+        out, lse = csa.gqa_dense_paged(q, cache, c.batch, c.scale)
+        csa.gqa_cache_mass(q, lse, cache, c.batch, c.scale)
+        kept, new_len = csa.gqa_cache_evict(cache, c.batch, 40, new, sink=2, recent=5)
+        return out, lse, kept, new_len
+
+    eager, captured = pool(), pool()
+    want = step(eager)
+    backup = [t.clone() for t in (captured.k, captured.v, captured.mass)]
+    graph = torch.cuda.CUDAGraph()
+    step(captured)  # what a first call loads is loaded before the capture
+    with torch.cuda.graph(graph):
+        got = step(captured)
+    for t, b in zip((captured.k, captured.v, captured.mass), backup):
+        t.copy_(b)
+    graph.replay()
+    torch.cuda.synchronize()
+    no_device_error()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for a, b in ((captured.k, eager.k), (captured.v, eager.v), (captured.mass, eager.mass)):
+        assert torch.equal(torch.nan_to_num(a, nan=9.0), torch.nan_to_num(b, nan=9.0))
+
+
+def test_two_calls_at_once():
+    cs = [Case(41 + i, [700, 60, 129], [40, 3, 1], 2, 4, (128, 128), 32) for i in range(2)]
+    qs = [c.q.to(DEV) for c in cs]
+    st = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            outs[i].append(csa.gqa_dense_paged(qs[i], cs[i].cache, cs[i].batch, cs[i].scale, stream=st[i]))
+    torch.cuda.synchronize()
+    no_device_error()
+    for i in range(2):
+        cs[i].check(*outs[i][0])
+        for out, lse in outs[i][1:]:
+            assert torch.equal(out, outs[i][0][0]) and torch.equal(lse, outs[i][0][1])
+
+
+@pytest.mark.parametrize("n", [1, 100])
+def test_outputs_and_scratch_on_16_byte_boundaries_only(n):
+    c = Case(43, [700], [n], 2, 4, (128, 128), 32)
+    buf = torch.empty(n * 8 * 128 + 8, dtype=torch.bfloat16, device=DEV)
+    out = buf[8:].view(n, 8, 128)
+    ws = torch.empty(csa.gqa_dense_workspace_size(n, 8, 2, 128) + 16, dtype=torch.uint8, device=DEV)[16:]
+    assert out.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+    c.check(*csa.gqa_dense_paged(c.q.to(DEV), c.cache, c.batch, c.scale, out=out, workspace=ws))
+    no_device_error()
+
+
+def test_pages_that_two_sequences_share():
+    # a common prefix of two pages; each sequence continues on its own
+    c = Case(44, [100, 100], [1, 1], 1, 4, (64, 64), 32)
+    c.table[1, :2] = c.table[0, :2]
+    c.batch.block_table.copy_(i32(c.table))
+    q = c.q.to(DEV)
+    out, lse = csa.gqa_dense_paged(q, c.cache, c.batch, c.scale)
+    c.check(out, lse)
+    before = f64(c.cache.mass)
+    got = f64(csa.gqa_cache_mass(q, lse, c.cache, c.batch, c.scale)) - before
+    add = [R.weights(f64(c.q[s:s + 1]), c.live(c.k, s), f64(lse[s:s + 1]), c.scale, 99)[0] for s in range(2)]
+    for pg in range(2):
+        want = add[0][32 * pg:32 * pg + 32] + add[1][32 * pg:32 * pg + 32]
+        assert np.allclose(got[c.table[0, pg], 0], want, rtol=0, atol=2.0**-21)  # three additions near 1 in fp32
+    no_device_error()
+
+
+def test_evicting_a_page_outside_the_pool_reads_zeros():
+    c = Case(45, [40], [0], 1, 1, (64, 64), 16)
+    table = c.table.copy()
+    table[0, 1] = 10**6
+    P = c.k.shape[0]
+    grow = [torch.cat([t, torch.full((2, *t.shape[1:]), 3.0, dtype=t.dtype)]).to(DEV) for t in (c.k, c.v, c.mass)]
+    cache = csa.GqaCache(*grow)
+    kept, _ = csa.gqa_cache_evict(cache, csa.GqaBatch(i32(table), i32([40]), None), 32, i32([[P, P + 1]]), recent=32)
+    torch.cuda.synchronize()
+    assert kept[0, 0].tolist() == list(range(8, 40))
+    assert torch.equal(cache.k[P, 0, :8].cpu(), c.k[table[0, 0], 0, 8:])
+    assert torch.all(cache.k[P, 0, 8:] == 0) and torch.all(cache.k[P + 1, 0, :8] == 0)
+    assert torch.equal(cache.k[P + 1, 0, 8:16].cpu(), c.k[table[0, 2], 0, :8])
+
+
+def test_wrong_tensors_are_refused():
+    c = Case(46, [40], [2], 2, 2, (64, 64), 16)
+    q = c.q.to(DEV)
+    call = lambda **kw: csa.gqa_dense_paged(**{**dict(q=q, cache=c.cache, batch=c.batch, scale=0.1), **kw})  # noqa: E731
+    with pytest.raises(ValueError, match="q must be"):
+        call(q=q.float())
+    with pytest.raises(ValueError, match="q must have shape"):
+        call(q=q[:1])
+    with pytest.raises(ValueError, match="contiguous"):
+        call(q=q.transpose(0, 1).contiguous().transpose(0, 1))
+    with pytest.raises(ValueError, match="cache.v"):
+        call(cache=csa.GqaCache(c.cache.k, c.cache.v[:, :1].contiguous()))
+    with pytest.raises(ValueError, match="block_table"):
+        call(batch=csa.GqaBatch(c.batch.block_table.long(), c.batch.cache_len, c.batch.cu_q, 2, 2))
+    with pytest.raises(ValueError, match="cache_len is on cpu"):
+        call(batch=csa.GqaBatch(c.batch.block_table, c.batch.cache_len.cpu(), c.batch.cu_q, 2, 2))
+    with pytest.raises(csa.CsaError, match="cu_q is NULL"):
+        call(batch=csa.GqaBatch(c.batch.block_table, c.batch.cache_len, None, 2, 2))
+    with pytest.raises(csa.CsaError, match="WORKSPACE"):
+        call(workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(csa.CsaError, match="mass"):
+        csa.gqa_cache_mass(q, torch.zeros(2, 4, device=DEV), csa.GqaCache(c.cache.k, c.cache.v), c.batch, 0.1)
+
+
 def test_on_another_stream():
     c = Case(32, [1000, 20], [30, 20], 2, 4, (128, 128), 32)
     st = torch.cuda.Stream()

@@ -163,6 +163,21 @@ def test_evict_refusals(lib, kw, word):
     assert st == INV and word in lib.csa_last_error(), lib.csa_last_error()
 
 
+def test_cpu_tensors_are_refused():
+    import torch
+
+    import long_context_sparse_10_b200 as csa
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t)  # noqa: E731
+    cache = csa.GqaCache(z(2, 1, 16, 64), z(2, 1, 16, 64), z(2, 1, 16, t=torch.float32))
+    bat = csa.GqaBatch(z(1, 1, t=torch.int32), z(1, t=torch.int32), z(2, t=torch.int32), 1, 1)
+    for call in (lambda: csa.gqa_dense_paged(z(1, 1, 64), cache, bat, 0.1),
+                 lambda: csa.gqa_cache_append(z(1, 1, 64), z(1, 1, 64), cache, bat),
+                 lambda: csa.gqa_cache_mass(z(1, 1, 64), z(1, 1, t=torch.float32), cache, bat, 0.1),
+                 lambda: csa.gqa_cache_evict(cache, bat, 16, z(1, 1, t=torch.int32))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
 def test_the_oracle_row_by_row():
     g = np.random.default_rng(0)
     q, k, v = g.standard_normal((3, 4, 8)), g.standard_normal((5, 2, 8)), g.standard_normal((5, 2, 6))
