@@ -230,10 +230,9 @@ __device__ __forceinline__ int stream_keys(const Geometry& g, const Walk& w, int
   const int tok = w.blk * g.tpb + (w.one ? 1 : s + 1) * g.tpt;
   return w.q.L - w.q.nq + (tok < w.q.nq ? tok : w.q.nq);
 }
-// Whether stream s clears the rows of V past the sequence's end in tile j: the first stream to use the tile.
-__device__ __forceinline__ bool clears_tail(bool one, int s, int j, int ks0, int L) {
-  return L - j * kTile < kTile && (one || s == 0 || ks0 <= j * kTile);
-}
+// Whether tile j holds keys past the sequence's end: each stream that works on it clears their rows of V before its own
+// product (zeros over zeros for the second).
+__device__ __forceinline__ bool clears_tail(int j, int L) { return L - j * kTile < kTile; }
 
 template <int DQK, int DV, bool PAGED, bool SINGLE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -384,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; more && healthy; more = w.next(g), ++items) {
       const bool one = w.one;
       const int t0 = w.t0, t1 = w.t1;
-      const int ks0 = stream_keys(g, w, 0), ks = s == 0 ? ks0 : stream_keys(g, w, 1);
+      const int ks = stream_keys(g, w, s);
       // its queries: tile s, or the one tile there is
       healthy = s == 0 || one ? wait_warp(&qfull[0], items & 1) : wait_warp(&qfull[1], pairs & 1);
       pairs += one ? 0 : 1;
@@ -404,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t kd = k_desc + __shfl_sync(0xffffffffu, sk * (S::kQBytes >> 4), 0);
         const uint64_t vd = v_desc + __shfl_sync(0xffffffffu, sv * (S::kVBytes >> 4), 0);
         if (j >= t0) healthy = wait_warp(&vfull[sv], (t / S::kVStages) & 1);
-        bar_arrive_if(&vland[s], lane == 0 && c > 0 && clears_tail(one, s, j, ks0, w.q.L));
+        bar_arrive_if(&vland[s], lane == 0 && c > 0 && clears_tail(j, w.q.L));
         if (c > 0 && fresh && items > 0) healthy = healthy && wait_warp(&oempty[s], (items - 1) & 1);
         if (c == 2) {
           healthy = healthy && wait_warp(&pfull[2 * s], parity & 1u);
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; more; more = w.next(g), ++items) {
       const bool one = w.one;
       const int off = w.q.L - w.q.nq;
-      const int ks0 = stream_keys(g, w, 0), ks = s == 0 ? ks0 : stream_keys(g, w, 1);
+      const int ks = stream_keys(g, w, s);
       const int tok = w.blk * g.tpb + (one ? 0 : s * g.tpt) + rt;
       const bool valid = row_used && tok < w.q.nq;
       // keys this row sees; a row that is not one is left unmasked (nobody reads its result)
@@ -536,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys past the sequence's end share its last tile: their values may be anything (another sequence,
         // a page never written), and 0 x NaN is NaN, so those rows of V become zeros.  The MMA warp, which
         // waits for every V tile in turn, says when this one is there.
-        if (clears_tail(one, s, j, ks0, w.q.L)) {
+        if (clears_tail(j, w.q.L)) {
           if (!wait_warp(&vland[s], tails & 1, limit)) limit = 1;
           ++tails;
           const int from = max(w.q.L - j * kTile, 0), n = (kTile - from) * 8;  // 16-byte pieces per column block

@@ -215,6 +215,20 @@ def test_one_long_sequence_is_shared_by_every_sm():
     assert torch.equal(out, again) and torch.equal(lse, lse2)  # partial states are joined in a fixed order
 
 
+def test_junk_behind_the_end_reaches_neither_of_two_row_tiles():
+    # every item has two tiles of rows over one key tile, whose end is junk (NaN): each stream's product waits for its
+    # own clearing, whichever of them comes first
+    lens = [33 + i % 60 for i in range(120)]
+    c = Case(8, lens, [L - i % 2 for i, L in enumerate(lens)], 2, 4, (128, 128), 64)
+    q = c.q.to(DEV)
+    runs = [csa.gqa_dense_paged(q, c.cache, c.batch, c.scale) for _ in range(40)]
+    torch.cuda.synchronize()
+    no_device_error()
+    c.check(*runs[0])
+    for out, lse in runs[1:]:
+        assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
+
+
 def test_many_sequences():
     g = np.random.default_rng(2)
     lens = [int(x) for x in g.integers(0, 90, 700)]
