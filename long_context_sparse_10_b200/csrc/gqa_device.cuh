@@ -147,15 +147,16 @@ struct Pool {
   float* mass;
   int64_t n_pages;
   int Hkv, page, kp, vp;  // kp, vp: pieces per token of k and v
+  int shift;              // page = 1 << shift
 };
 
 // Slot (row of the pool's planes) of a position, or -1 where the table holds no page of the pool for it.
 __device__ __forceinline__ int64_t slot_of(const Pool& c, const int32_t* table, int max_pages, int h, int pos) {
-  const int pg = pos / c.page;
+  const int pg = pos >> c.shift;
   if (pos < 0 || pg >= max_pages) return -1;
   const int id = __ldg(table + pg);
   if (id < 0 || id >= c.n_pages) return -1;
-  return (static_cast<int64_t>(id) * c.Hkv + h) * c.page + pos % c.page;
+  return ((static_cast<int64_t>(id) * c.Hkv + h) << c.shift) + (pos & (c.page - 1));
 }
 
 inline Pool pool_of(const gqa_cache* c) {
@@ -166,6 +167,7 @@ inline Pool pool_of(const gqa_cache* c) {
   p.n_pages = c->n_pages;
   p.Hkv = c->n_kv_heads;
   p.page = c->page_size;
+  p.shift = c->page_size == 16 ? 4 : (c->page_size == 32 ? 5 : (c->page_size == 64 ? 6 : 7));
   p.kp = c->d_qk / 8;
   p.vp = c->d_v / 8;
   return p;
