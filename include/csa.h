@@ -513,7 +513,8 @@ CSA_API csa_status csa_grouped_out_proj(const void* o, int64_t R, int32_t H, int
  *   v    bf16 [n_pages, H_kv, page_size, d_v]
  *   mass fp32 [n_pages, H_kv, page_size], nullable: the accumulated attention
  *        weight of each cached token (gqa_cache_mass, gqa_cache_evict)
- *   page_size 16, 32, 64 or 128;  n_pages * H_kv * page_size < 2^31 - 128
+ *   page_size 16, 32, 64 or 128;  n_pages * H_kv * page_size < 2^31 - 128,
+ *   max_pages (of a batch) * page_size < 2^31 - 65536
  */
 typedef struct gqa_cache {
   void* k;

@@ -71,6 +71,7 @@ struct EvictParams {
 };
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kRun = 4 * kSelThreads;  // positions a block takes at a time, four a thread
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxHeld = 49152;  // keys a block can hold (192 KB)
@@ -98,35 +99,20 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
     return;
   }
   const int lo = p.sink, hi = L - p.recent, want = p.budget - p.sink - p.recent;
-  // this block's positions [a, b); runs of 512 split evenly among the warps
-  const int per = (L + ranks * kSelThreads - 1) / (ranks * kSelThreads) * kSelThreads;
+  // this block's positions [a, b), split evenly among the warps
+  const int per = (L + ranks * kRun - 1) / (ranks * kRun) * kRun;
   const int a = min(rank * per, L), b = min(a + per, L);
   const bool held = per <= p.held;
-  auto key_of = [&](int j) -> uint32_t {
+  // keys of positions j .. j + 3 (j a multiple of 4: one page, on a 16-byte boundary)
+  auto read4 = [&](int j) -> uint4 {
     const int64_t at = slot_of(p.c, table, p.max_pages, h, j);
-    return mass_key(at < 0 ? 0.f : p.c.mass[at]);
+    const float4 m = at < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(p.c.mass + at);
+    return make_uint4(mass_key(m.x), mass_key(m.y), mass_key(m.z), mass_key(m.w));
   };
+  auto keys4 = [&](int j) -> uint4 { return held ? *reinterpret_cast<const uint4*>(keys + (j - a)) : read4(j); };
   if (held) {
-    // four positions lie in one page, on a 16-byte boundary; four such loads in flight
-    for (int j0 = a + 4 * tid; j0 < b; j0 += 16 * kSelThreads) {
-      int64_t at[4];
-      float4 m[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = j0 + 4 * u * kSelThreads;
-        at[u] = j < b ? slot_of(p.c, table, p.max_pages, h, j) : -1;
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        m[u] = at[u] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(p.c.mass + at[u]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = j0 + 4 * u * kSelThreads;
-        if (j < b)
-          *reinterpret_cast<uint4*>(keys + (j - a)) =
-              make_uint4(mass_key(m[u].x), mass_key(m[u].y), mass_key(m[u].z), mass_key(m[u].w));
-      }
-    }
+#pragma unroll 4
+    for (int j = a + 4 * tid; j < b; j += kRun) *reinterpret_cast<uint4*>(keys + (j - a)) = read4(j);
   }
   uint32_t prefix = 0;
   int need = want;  // of the keys that share the prefix
@@ -137,9 +123,15 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
       const uint32_t mask = round == 0 ? 0u : ~0u << (round == 1 ? 21 : 10);
       for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int j = max(a, lo) + tid; j < min(b, hi); j += kSelThreads) {
-        const uint32_t k = held ? keys[j - a] : key_of(j);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+      const int from = max(a, lo), to = min(b, hi);
+#pragma unroll 4
+      for (int j = a + 4 * tid; j < b; j += kRun) {
+        const uint4 k4 = keys4(j);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (j + u >= from && j + u < to && (k[u] & mask) == prefix)
+            atomicAdd(&hist[(k[u] >> shift) & ((1u << bits) - 1u)], 1);
       }
       cluster.sync();
       // the cluster's sums: each block adds up a part of the bins and gives it to all
@@ -184,27 +176,31 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
     }
   }
   // kept: sink, recent, keys above the cut, and the first `need` keys equal to it
-  const int seg = per / kSelWarps;  // positions per warp, a multiple of 32
+  const int seg = per / kSelWarps;  // positions per warp, a multiple of 128
   const int wa = min(a + warp * seg, b), wb = min(wa + seg, b);
-  auto classify = [&](int j, bool& gt, bool& eq) {
-    gt = eq = false;
+  auto classify = [&](int j, uint32_t& gt, uint32_t& eq) {  // a bit for each of positions j .. j + 3
+    gt = eq = 0;
     if (j >= wb) return;
-    if (j < lo || j >= hi) {
-      gt = true;
-    } else if (want > 0) {
-      const uint32_t k = held ? keys[j - a] : key_of(j);
-      gt = k > prefix;
-      eq = k == prefix;
+    const uint4 k4 = keys4(j);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (j + u >= wb) break;
+      const bool ends = j + u < lo || j + u >= hi;
+      gt |= (ends || (want > 0 && k[u] > prefix)) ? 1u << u : 0u;
+      eq |= (!ends && want > 0 && k[u] == prefix) ? 1u << u : 0u;
     }
   };
   __syncthreads();
   int ngt = 0, neq = 0;
-  for (int j = wa; j < wb; j += 32) {
-    bool gt, eq;
-    classify(j + lane, gt, eq);
-    ngt += __popc(__ballot_sync(0xffffffffu, gt));
-    neq += __popc(__ballot_sync(0xffffffffu, eq));
+  for (int j = wa; j < wb; j += 128) {
+    uint32_t gt, eq;
+    classify(j + 4 * lane, gt, eq);
+    ngt += __popc(gt);
+    neq += __popc(eq);
   }
+  ngt = warp_sum_i(ngt);
+  neq = warp_sum_i(neq);
   if (lane == 0) {
     warp_gt[warp] = ngt;
     warp_eq[warp] = neq;
@@ -230,17 +226,29 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
     eq_at += warp_eq[w];
   }
   out_at += min(eq_at, need);
-  for (int j = wa; j < wb; j += 32) {
-    bool gt, eq;
-    classify(j + lane, gt, eq);
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t me = __ballot_sync(0xffffffffu, eq);
-    const bool take = gt || (eq && eq_at + __popc(me & below) < need);
-    const uint32_t mt = __ballot_sync(0xffffffffu, take);
-    const int at = out_at + __popc(mt & below);
-    if (take && at < p.budget) kept[at] = j + lane;
-    eq_at += __popc(me);
-    out_at += __popc(mt);
+  for (int j = wa; j < wb; j += 128) {
+    uint32_t gt, eq;
+    classify(j + 4 * lane, gt, eq);
+    const int mine = __popc(gt) | (__popc(eq) << 16);
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const int all = __shfl_sync(0xffffffffu, inc, 31);
+    const int open = max(need - eq_at, 0);  // equal keys still to be kept
+    int eq_before = (inc - mine) >> 16;
+    int at = out_at + ((inc - mine) & 0xffff) + min(open, eq_before);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool e = (eq >> u) & 1u, take = ((gt >> u) & 1u) || (e && eq_before < open);
+      if (take && at < p.budget) kept[at] = j + 4 * lane + u;
+      at += take ? 1 : 0;
+      eq_before += e ? 1 : 0;
+    }
+    out_at += (all & 0xffff) + min(open, all >> 16);
+    eq_at += all >> 16;
   }
   cluster.sync();  // no block leaves while another may read its counts
 }
@@ -369,7 +377,7 @@ csa_status gqa_cache_evict(const gqa_cache* cache, const gqa_batch* batch, int32
   const int longest = batch->max_pages * cache->page_size;
   int ranks = 1;
   while (ranks < kMaxCluster && longest > 4096 * ranks) ranks *= 2;
-  p.held = (longest + ranks * kSelThreads - 1) / (ranks * kSelThreads) * kSelThreads;
+  p.held = static_cast<int>((static_cast<int64_t>(longest) + ranks * kRun - 1) / (ranks * kRun) * kRun);
   if (p.held > kMaxHeld) p.held = 0;  // read again each time
   const int smem = p.held * 4;
   if (!ensure_smem(reinterpret_cast<const void*>(gqa_evict_select_kernel), smem))

@@ -64,8 +64,8 @@ inline csa_status check_pool(const char* what, const gqa_cache* cache, const gqa
                   cache->n_pages < ((int64_t(1) << 31) - 128) / (static_cast<int64_t>(cache->n_kv_heads) * cache->page_size),
               "%s: n_pages must be at least 1, and n_pages * H_kv * page_size below 2^31 - 128", what);
   CSA_REQUIRE(batch->max_pages >= 1, "%s: max_pages must be at least 1", what);
-  CSA_REQUIRE(static_cast<int64_t>(batch->max_pages) * cache->page_size < (int64_t(1) << 31) - 256,
-              "%s: max_pages * page_size must be below 2^31 - 256", what);
+  CSA_REQUIRE(static_cast<int64_t>(batch->max_pages) * cache->page_size < (int64_t(1) << 31) - 65536,
+              "%s: max_pages * page_size must be below 2^31 - 65536", what);
   CSA_REQUIRE_PTR(cache->k);
   CSA_REQUIRE_PTR(cache->v);
   CSA_REQUIRE_PTR(batch->block_table);
