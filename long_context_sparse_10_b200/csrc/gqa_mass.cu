@@ -9,9 +9,10 @@
 // (sequence, kv head); it walks over the row blocks that see it, each Q block
 // serving both tiles.  gqa_work.cuh shares the items out by their cost.
 //
-// Bound: one new token per sequence reads K once (HBM); many rows cost one
-// exponential per (key, row), which the exponential unit gives at 16 a clock
-// and SM.
+// Bound: one new token per sequence reads K once (HBM; 16 sequences of 1500 to
+// 16384 tokens, 302 MB: 56 us, 0.82 of the measured copy bandwidth); many rows
+// cost one exponential per (key, row), which the exponential unit gives at 16 a
+// clock and SM.
 //
 // Roles of a CTA (one per SM, 320 threads): warps 0-3 and 4-7 take the two key
 // tiles (two score buffers of 128 TMEM columns each), warp 8 loads by TMA, warp
