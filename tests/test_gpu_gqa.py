@@ -165,6 +165,7 @@ PAGED = [
     ([600, 64], [2, 3], 1, 128, (64, 64), 64),
     ([5000], [1], 1, 16, (192, 128), 64),
     ([900, 900], [64, 1], 3, 12, (128, 128), 128),
+    ([190, 3], [5, 1], 1, 50, (128, 128), 16),
 ]
 
 
@@ -500,6 +501,7 @@ MASS = [
     ([600, 64], [2, 3], 1, 128, (64, 64), 64),
     ([3, 20], [5, 20], 1, 2, (128, 128), 16),
     ([900, 900], [64, 1], 3, 12, (128, 128), 128),
+    ([190, 3], [5, 1], 1, 50, (128, 128), 16),
 ]
 
 
