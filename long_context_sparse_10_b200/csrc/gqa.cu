@@ -238,6 +238,11 @@ __device__ __forceinline__ int steps_of(bool one, int s, int j, int ks) {
   if ((one && (j & 1) != s) || left <= 0) return 0;
   return left > kStep ? 2 : 1;
 }
+// Whether stream s has a tile of [t0, t1): its first one (it works on them up to its last row's keys).
+__device__ __forceinline__ bool takes_part(bool one, int s, int t0, int t1, int ks) {
+  const int j = one ? t0 + ((t0 & 1) ^ s) : t0;
+  return j < t1 && ks > j * kTile;
+}
 // Keys the last row of stream s sees.
 __device__ __forceinline__ int stream_keys(const Geometry& g, const Walk& w, int s) {
   const int tok = w.blk * g.tpb + (w.one ? 1 : s + 1) * g.tpt;
@@ -392,13 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool healthy = true;
     int items = 0, pairs = 0;
     int base = 0;             // this CTA's tiles before the item
+    int parts = 0;            // items the stream took part in
     uint32_t parity = 0;      // of pfull[s][half], a bit each
     for (; more && healthy; more = w.next(g), ++items) {
       const bool one = w.one;
       const int t0 = w.t0, t1 = w.t1;
       const int ks = stream_keys(g, w, s);
       // its queries: tile s, or the one tile there is
-      healthy = s == 0 || one ? wait_warp(&qfull[0], items & 1) : wait_warp(&qfull[1], pairs & 1);
+      healthy = wait_warp(&qfull[0], items & 1);
+      if (s == 1 && !one) healthy = healthy && wait_warp(&qfull[1], pairs & 1);
       pairs += one ? 0 : 1;
       const uint64_t qd = q_desc + (one ? 0 : __shfl_sync(0xffffffffu, s * (S::kQBytes >> 4), 0));
       const int ahead = one ? 2 : 1;  // tiles to the stream's next
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vd = v_desc + __shfl_sync(0xffffffffu, sv * (S::kVBytes >> 4), 0);
         if (j >= t0) healthy = wait_warp(&vfull[sv], (t / S::kVStages) & 1);
         bar_arrive_if(&vland[s], lane == 0 && c > 0 && clears_tail(j, w.q.L));
-        if (c > 0 && fresh && items > 0) healthy = healthy && wait_warp(&oempty[s], (items - 1) & 1);
+        if (c > 0 && fresh && parts > 0) healthy = healthy && wait_warp(&oempty[s], (parts - 1) & 1);
         if (c == 2) {
           healthy = healthy && wait_warp(&pfull[2 * s], parity & 1u);
           parity ^= 1u;
@@ -464,9 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (c > 0) fresh = false;
       }
-      // a stream without a tile here: its previous item's read-out is awaited all the same, so that no phase of
-      // oempty is left two behind
-      if (items > 0 && healthy && fresh) healthy = wait_warp(&oempty[s], (items - 1) & 1);
+      parts += takes_part(one, s, t0, t1, ks) ? 1 : 0;
       base += t1 - t0;
     }
   } else if (warp == 11) {
@@ -649,8 +654,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc::fence_before_sync();
-        bar_arrive(&oempty[s]);
-        if (one) bar_arrive(&oempty[1]);
+        // the next item in which a stream takes part may overwrite its O
+        bar_arrive_if(&oempty[s], any);
+        bar_arrive_if(&oempty[1], one && takes_part(true, 1, w.t0, w.t1, ks));
       }
       base += w.t1 - w.t0;
     }

@@ -88,9 +88,6 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "f"(a0), "f"(a1));
 }
 
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
 // Wait of a converged warp for a barrier's phase.  Almost always the phase is there or arrives within one try: that
 // path has one try and a vote, so that no branch of it diverges (a loop whose exit is each lane's own costs 150
 // clocks more).  The bounded loop is for the rest; false, for all lanes, when it runs out.

@@ -230,6 +230,20 @@ def test_junk_behind_the_end_reaches_neither_of_two_row_tiles():
         assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
 
 
+def test_items_in_which_a_stream_has_no_tile():
+    # one-tile items give the second stream nothing, and so do rows whose keys end before a CTA's piece; no wait may
+    # depend on which stream runs ahead
+    for seed, (L, n) in enumerate(((100, 1), (128, 1), (129, 2), (40, 40), (300, 70))):
+        lens = [max(n, L - i % 7) for i in range(300)]
+        c = Case(50 + seed, lens, [n] * 300, 1, 4, (64, 64), 16)
+        q = c.q.to(DEV)
+        runs = [csa.gqa_dense_paged(q, c.cache, c.batch, c.scale) for _ in range(60)]
+        torch.cuda.synchronize()
+        no_device_error()
+        for out, lse in runs[1:]:
+            assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
+
+
 def test_many_sequences():
     g = np.random.default_rng(2)
     lens = [int(x) for x in g.integers(0, 90, 700)]
