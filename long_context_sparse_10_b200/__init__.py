@@ -535,18 +535,29 @@ def gqa_dense_workspace_size(max_q, H, H_kv, d_v) -> int:
     return int(_lib.load().gqa_dense_workspace_size(max_q, H, H_kv, d_v))
 
 
-def _gqa_buffers(lib, q, d_v, max_q, H_kv, out, lse, workspace):
-    R, H, _ = q.shape
+def _gqa_buffers(lib, q, shape, d_v, max_q, H_kv, out, lse, workspace):
+    """Output, lse and workspace of a call (those not given are allocated) with their addresses, and the workspace's
+    size."""
+    R, H, _ = shape
     dev = q.device
     if out is None:
-        out = torch.empty((R, H, d_v), dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((R, H, d_v))
+        op = out.data_ptr()
+    else:
+        op = _tensor(out, "out", torch.bfloat16, (R, H, d_v), dev)
     if lse is None:
         lse = torch.empty((R, H), dtype=torch.float32, device=dev)
+        lp = lse.data_ptr()
+    else:
+        lp = _tensor(lse, "lse", torch.float32, (R, H), dev)
     if workspace is None:
-        workspace = torch.empty(lib.gqa_dense_workspace_size(max_q, H, H_kv, d_v), dtype=torch.uint8, device=dev)
-    return (out, lse, workspace, _tensor(out, "out", torch.bfloat16, (R, H, d_v), dev),
-            _tensor(lse, "lse", torch.float32, (R, H), dev),
-            _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), dev))
+        size = lib.gqa_dense_workspace_size(max_q, H, H_kv, d_v)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        wp = workspace.data_ptr()
+    else:
+        size = workspace.numel()
+        wp = _tensor(workspace, "workspace", torch.uint8, (size,), dev)
+    return out, lse, workspace, op, lp, wp, size
 
 
 def gqa_dense_packed(q, k, v, packed: Packed, scale, *, out=None, lse=None, workspace=None, stream=None):
@@ -564,9 +575,10 @@ def gqa_dense_packed(q, k, v, packed: Packed, scale, *, out=None, lse=None, work
     vp = _tensor(v, "v", torch.bfloat16, (R, H_kv, d_v), dev)
     if packed.cu_tokens.device != dev:
         raise ValueError(f"the packed offsets are on {packed.cu_tokens.device}, not on {dev}")
-    out, lse, workspace, op, lp, wp = _gqa_buffers(lib, q, d_v, packed.max_tokens, H_kv, out, lse, workspace)
-    _check(lib.gqa_dense_packed(qp, kp, vp, ctypes.byref(packed.desc()), H, H_kv, d_qk, d_v, scale, op, lp, wp,
-                                workspace.numel(), _current_stream(dev)), "gqa_dense_packed")
+    out, lse, workspace, op, lp, wp, size = _gqa_buffers(lib, q, (R, H, d_qk), d_v, packed.max_tokens, H_kv, out, lse,
+                                                         workspace)
+    _check(lib.gqa_dense_packed(qp, kp, vp, ctypes.byref(packed.desc()), H, H_kv, d_qk, d_v, scale, op, lp, wp, size,
+                                _current_stream(dev)), "gqa_dense_packed")
     return out, lse
 
 
@@ -579,10 +591,12 @@ def gqa_dense_paged(q, cache: GqaCache, batch: GqaBatch, scale, *, out=None, lse
             return gqa_dense_paged(q, cache, batch, scale, out=out, lse=lse, workspace=workspace)
     lib = _lib.load()
     cd, bd = cache.desc(dev), batch.desc(dev)
-    qp = _tensor(q, "q", torch.bfloat16, (batch.total_q, _dims(q, 3, "q")[1], cd.d_qk), dev)
-    out, lse, workspace, op, lp, wp = _gqa_buffers(lib, q, cd.d_v, batch.max_q, cd.n_kv_heads, out, lse, workspace)
-    _check(lib.gqa_dense_paged(qp, ctypes.byref(cd), ctypes.byref(bd), q.shape[1], scale, op, lp, wp,
-                               workspace.numel(), _current_stream(dev)), "gqa_dense_paged")
+    shape = (batch.total_q, _dims(q, 3, "q")[1], cd.d_qk)
+    qp = _tensor(q, "q", torch.bfloat16, shape, dev)
+    out, lse, workspace, op, lp, wp, size = _gqa_buffers(lib, q, shape, cd.d_v, batch.max_q, cd.n_kv_heads, out, lse,
+                                                         workspace)
+    _check(lib.gqa_dense_paged(qp, ctypes.byref(cd), ctypes.byref(bd), shape[1], scale, op, lp, wp, size,
+                               _current_stream(dev)), "gqa_dense_paged")
     return out, lse
 
 

@@ -257,7 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     gqa_attn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using S = Shape<DQK, DV, SINGLE>;
-  pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* Qs = smem;
@@ -281,7 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Geometry& g = p.g;
 
+  // barriers, maps and TMEM need nothing of the kernel before; its results are first read by the partition
   if (tid == 0) {
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
     busy[0] = busy[1] = 0;
     for (int i = 0; i < S::kKStages; ++i) {
       tc::bar_init(&kfull[i], 1);
@@ -304,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::bar_init_fence();
   }
   if (warp == 9) tc::tmem_alloc(tslot, 512);
+  pdl_wait();
   const gqa::Share share = gqa::find_share<gqa::Blocks>(g, blockIdx.x, gridDim.x, scratch);
   Walk w;
   bool more = w.begin(g, share);
@@ -661,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       base += w.t1 - w.t0;
     }
     if (tid == 0) p.meta[blockIdx.x].x = flags;
+    pdl_trigger();  // only the merge is left
   }
   tc::fence_before_sync();
   __syncthreads();

@@ -28,6 +28,7 @@ struct AppendParams {
 
 __global__ void __launch_bounds__(256) gqa_append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= p.total_q || row >= __ldg(p.cu_q + p.n_seqs)) return;
@@ -85,6 +86,7 @@ __device__ __forceinline__ uint32_t mass_key(float m) { return m != m ? 0xffffff
 
 __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __grid_constant__ EvictParams p) {
   pdl_wait();
+  pdl_trigger();
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ int hist[kBins], total[kBins];

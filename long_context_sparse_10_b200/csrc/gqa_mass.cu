@@ -116,7 +116,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     gqa_mass_kernel(const __grid_constant__ MassParams p, const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kmap) {
   using S = MassShape<DQK>;
-  pdl_wait();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem);
@@ -134,6 +133,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Geometry& g = p.g;
 
   if (tid == 0) {
+    prefetch_map(&qmap);
+    prefetch_map(&kmap);
     for (int i = 0; i < S::kMaxStages; ++i) {
       tc::bar_init(&kfull[i], 1);
       tc::bar_init(&kempty[i], 1);
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::bar_init_fence();
   }
   if (warp == 9) tc::tmem_alloc(tslot, 512);
+  pdl_wait();  // nothing above depends on the kernel before
   const Share share = find_share<KeyPairs>(g, blockIdx.x, gridDim.x, reinterpret_cast<int64_t*>(consts));
   MassWalk w;
   bool more = w.begin(g, share);
@@ -315,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the only addition of this call to the token, unless sequences share the page
       if (at >= 0) atomicAdd(p.c.mass + at, sum);
     }
+    pdl_trigger();
   }
   tc::fence_before_sync();
   __syncthreads();
