@@ -680,61 +680,62 @@ template <int DV, int ROWS>
 __global__ void __launch_bounds__(256) gqa_merge_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int4 me = p.meta[c];
-  if (!(me.x & kMetaOwner)) return;
+  // every load that needs no other is made first: lane i holds what CTA c - i left
+  int4 info = p.meta[max(c - lane, 0)];
+  const int flags = __shfl_sync(0xffffffffu, info.x, 0);
+  if (!(flags & kMetaOwner)) return;
+  const int s = __shfl_sync(0xffffffffu, info.y, 0), h = __shfl_sync(0xffffffffu, info.z, 0);
+  const int blk = __shfl_sync(0xffffffffu, info.w, 0);
   const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int tile = row / kTile, r = row % kTile;
   const int rt = r / p.g.G, rg = r - rt * p.g.G;
   Seq q;
-  q.load(p.g, me.y);
-  const int tok = me.w * p.g.tpb + tile * p.g.tpt + rt;
+  q.load(p.g, s);
+  const int tok = blk * p.g.tpb + tile * p.g.tpt + rt;
   if (rt >= p.g.tpt || tok >= q.nq) return;
-  int begin = c - 1;  // the CTA in which the item begins
-  while (begin > 0 && !(p.meta[begin].x & kMetaBegins)) --begin;
-  const int n = c - begin + 1;
-  auto slot = [&](int i) -> int64_t {  // piece i, counted back from CTA c
-    const int b = c - i;
-    const int second = (i > 0 && !(p.meta[b].x & kMetaSingle)) ? 1 : 0;
-    return (static_cast<int64_t>(2) * b + second) * ROWS + row;
-  };
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, p.ml[slot(i)].x);
-  top = warp_max(top);
-  const float ref = top == -INFINITY ? 0.f : top;
+  float top = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float wgt = 0.f, li = 0.f;
-    int64_t at = 0;
-    if (i0 + lane < n) {
-      at = slot(i0 + lane);
-      const float2 ml = p.ml[at];
-      wgt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - ref);
-      li = ml.y * wgt;
-    }
-    const int m = min(32, n - i0);
+  // pieces c, c - 1, ... down to the nearest CTA below c whose last piece begins the item, 32 at a time
+  for (int i0 = 0;; i0 += 32) {
+    const int i = i0 + lane, from = c - i;
+    if (i0 > 0) info = p.meta[max(from, 0)];
+    const uint32_t begins = __ballot_sync(0xffffffffu, i > 0 && (from <= 0 || (info.x & kMetaBegins)));
+    const int n = begins ? __ffs(begins) : 32;  // pieces here
+    const int second = (i > 0 && !(info.x & kMetaSingle)) ? 1 : 0;
+    const int64_t slot = (static_cast<int64_t>(2) * max(from, 0) + second) * ROWS + row;
+    const float2 ml = lane < n ? p.ml[slot] : make_float2(-INFINITY, 0.f);
+    const float now = fmaxf(top, warp_max(ml.x)), ref = now == -INFINITY ? 0.f : now;
+    const float old = top == -INFINITY ? 0.f : exp2f(top - ref);
+    const float wgt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - ref);
+    top = now;
+    l *= old;
+    acc.x *= old;
+    acc.y *= old;
+    acc.z *= old;
+    acc.w *= old;
+    const float li = ml.y * wgt;
 #pragma unroll 4
-    for (int i = 0; i < m; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, wgt, i);
-      l += __shfl_sync(0xffffffffu, li, i);
-      const int64_t a = __shfl_sync(0xffffffffu, at, i);
-      if (lane < DV / 4 && wi != 0.f) {
-        const float4 o = *reinterpret_cast<const float4*>(p.part + a * DV + 4 * lane);
-        acc.x += o.x * wi;
-        acc.y += o.y * wi;
-        acc.z += o.z * wi;
-        acc.w += o.w * wi;
-      }
+    for (int u = 0; u < n; ++u) {
+      const int64_t at = __shfl_sync(0xffffffffu, slot, u);
+      // (a piece without a key of this row holds zeros)
+      const float4 o = lane < DV / 4 ? *reinterpret_cast<const float4*>(p.part + at * DV + 4 * lane)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float wi = __shfl_sync(0xffffffffu, wgt, u);
+      l += __shfl_sync(0xffffffffu, li, u);
+      acc.x += o.x * wi;
+      acc.y += o.y * wi;
+      acc.z += o.z * wi;
+      acc.w += o.w * wi;
     }
+    if (begins) break;
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  const int64_t grow = static_cast<int64_t>(q.row0 + tok) * p.Hq + me.z * p.g.G + rg;
+  const int64_t grow = static_cast<int64_t>(q.row0 + tok) * p.Hq + h * p.g.G + rg;
   if (lane < DV / 4)
     *reinterpret_cast<uint2*>(p.out + grow * DV + 4 * lane) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (lane == 0 && p.lse != nullptr) p.lse[grow] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
-
 
 struct Workspace {
   size_t part, ml, meta, bytes;
