@@ -141,24 +141,27 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
             atomicAdd(&hist[(k[u] >> shift) & ((1u << bits) - 1u)], 1);
       }
       cluster.sync();
-      // the cluster's sums: each block adds up a part of the bins and gives it to all
-      const int part = kBins / ranks;
-      for (int i = rank * part + tid; i < (rank + 1) * part; i += kSelThreads) {
-        int c[kMaxCluster], sum = 0;
+      if (ranks > 1) {
+        // the cluster's sums: each block adds up a part of the bins and gives it to all
+        const int part = kBins / ranks;
+        for (int i = rank * part + tid; i < (rank + 1) * part; i += kSelThreads) {
+          int c[kMaxCluster], sum = 0;
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) c[r] = r < ranks ? *cluster.map_shared_rank(&hist[i], r) : 0;
+          for (int r = 0; r < kMaxCluster; ++r) c[r] = r < ranks ? *cluster.map_shared_rank(&hist[i], r) : 0;
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) sum += c[r];
+          for (int r = 0; r < kMaxCluster; ++r) sum += c[r];
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          if (r < ranks) *cluster.map_shared_rank(&total[i], r) = sum;
+          for (int r = 0; r < kMaxCluster; ++r)
+            if (r < ranks) *cluster.map_shared_rank(&total[i], r) = sum;
+        }
+        cluster.sync();
       }
-      cluster.sync();
+      const int* sums = ranks > 1 ? total : hist;
       // thread t holds bins 2047 - 4 t down to 2044 - 4 t
       int c4[4], mine = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        c4[i] = total[kBins - 1 - 4 * tid - i];
+        c4[i] = sums[kBins - 1 - 4 * tid - i];
         mine += c4[i];
       }
       int inc = mine;
