@@ -307,6 +307,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::bar_init_fence();
   }
   if (warp == 9) tc::tmem_alloc(tslot, 512);
+  // Rows of the Q tiles that no token fills stay zero, and with them their scores and (overlaid) probabilities: the
+  // MMAs of a decode step, 8 rows of 128 in use, then burn less power, which is what the clocks hang on.
+  const uint32_t rows_q = static_cast<uint32_t>(g.tpt * g.G);
+  for (int i = tid; i < S::kQTiles * S::kQc * (kTile - static_cast<int>(rows_q)) * 8; i += kThreads) {
+    const int per = (kTile - static_cast<int>(rows_q)) * 8, c = i / per;
+    *reinterpret_cast<uint4*>(Qs + c * (kTile * 128) + rows_q * 128 + (i - c * per) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  tc::fence_async_smem();
   pdl_wait();
   const gqa::Share share = gqa::find_share<gqa::Blocks>(g, blockIdx.x, gridDim.x, scratch);
   Walk w;
@@ -315,7 +323,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tslot;
-  const uint32_t rows_q = static_cast<uint32_t>(g.tpt * g.G);
 
   if (warp == 8) {
     regs_down();
@@ -786,6 +793,9 @@ csa_status dispatch(const char* what, Params& p, const gqa::Heads& h, const CUte
   return fail(CSA_ERR_UNSUPPORTED, "%s: channel widths %d/%d", what, h.dqk, h.dv);
 }
 
+// Tokens of a row tile: what 128 rows hold, or a sequence brings.
+int tokens_per_tile(int G, int64_t max_q) { return static_cast<int>(kTile / G < max_q ? kTile / G : max_q); }
+
 // No item of any sequence has more rows than this.
 int64_t rows_bound(int64_t max_q, int64_t G) { return max_q > 2 * kTile ? 2 * kTile : (max_q * G > 2 * kTile ? 2 * kTile : max_q * G); }
 
@@ -857,7 +867,7 @@ csa_status gqa_dense_packed(const void* q, const void* k, const void* v, const c
   p.g.total_q = packed->total_tokens;
   p.g.Hkv = h.Hkv;
   p.g.G = h.G;
-  p.g.tpt = kTile / h.G;
+  p.g.tpt = tokens_per_tile(h.G, packed->max_tokens);
   p.page = kTile;
   CUtensorMap qm, km, vm;
   const uint64_t rows = static_cast<uint64_t>(packed->total_tokens);
@@ -892,7 +902,7 @@ csa_status gqa_dense_paged(const void* q, const gqa_cache* cache, const gqa_batc
   p.g.total_q = batch->total_q;
   p.g.Hkv = h.Hkv;
   p.g.G = h.G;
-  p.g.tpt = kTile / h.G;
+  p.g.tpt = tokens_per_tile(h.G, batch->max_q);
   p.block_table = batch->block_table;
   p.max_pages = batch->max_pages;
   p.page = cache->page_size;
