@@ -39,8 +39,8 @@
 // operands.
 //
 // Measured (B200, 8192-token prompt, 32 query and 8 kv heads of 128 channels,
-// 550 GFLOP): 540 us in short runs at 1.9 GHz (0.62 of the measured bf16 peak),
-// 607 us in a sustained run at the power cap; the tensor pipe is active half the
+// 550 GFLOP): 530 us in short runs at 1.9 GHz (0.63 of the measured bf16 peak),
+// 605 us in a sustained run at the power cap; the tensor pipe is active half the
 // time.  A 128-key tile takes a stream about 3900 clocks: 2400 of softmax (two
 // warps share a scheduler's exponential and fp32 units), 770 of MMAs, the rest
 // hand-overs: a barrier operation costs 100 to 250 clocks while the score MMAs
