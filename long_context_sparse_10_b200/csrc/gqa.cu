@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_down();
     // ===================== TMA producer =====================
     bool healthy = true;
-    int items = 0, tk = 0, tv = 0;
+    int items = 0, tk = 0, tv = 0, q_loads[2] = {0, 0};
     for (; more && healthy; more = w.next(g), ++items) {
       // a tile's 128 rows: one box (prompts), or one box per page and 64-channel block
       const int live = PAGED ? (w.q.L + p.page - 1) / p.page : 0;
@@ -374,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         healthy = wait_warp(&qempty[0], (items - 1) & 1) && wait_warp(&qempty[1], (items - 1) & 1);
         if (!healthy) break;
       }
+      ++q_loads[0];
+      q_loads[1] += w.one ? 0 : 1;
       if (lane == 0) {
         const int nt = w.one ? 1 : 2;
         for (int s = 0; s < nt; ++s) {
@@ -393,6 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (healthy) healthy = load_tile(true, j, row_cur);
         row_cur = row_next;
       }
+    }
+    if (!healthy) {
+      await_copies(kfull, S::kKStages, tk);
+      await_copies(vfull, S::kVStages, tv);
+      await_copies(&qfull[0], 1, q_loads[0]);
+      await_copies(&qfull[1], 1, q_loads[1]);
     }
   } else if (warp == 9 || warp == 10) {
     regs_down();

@@ -102,6 +102,12 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32
   if (!all) all = __all_sync(0xffffffffu, tc::bar_wait_bounded(bar, parity, limit));
   return all;
 }
+// After a wait has run out: waits, with a limit, for the copies still in flight into a ring of `stages`, of which
+// `loads` were issued.
+__device__ __forceinline__ void await_copies(uint64_t* full, int stages, int loads) {
+#pragma unroll 1
+  for (int st = 0; st < stages && st < loads; ++st) wait_warp(&full[st], ((loads - 1 - st) / stages) & 1, 1u << 14);
+}
 // Arrives where `on` holds, without a branch.
 __device__ __forceinline__ void bar_arrive_if(uint64_t* bar, bool on, uint32_t n = 1) {
   asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 _, [%0], %2;\n}\n" ::"r"(

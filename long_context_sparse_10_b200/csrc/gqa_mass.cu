@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     // ===================== TMA producer =====================
     Ring kr, qr;
+    int k_loads = 0, q_loads = 0;
     bool healthy = true;
     const int ppt = kTile / p.c.page;
     for (; more && healthy; more = w.next(g)) {
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           &kfull[kr.st]);
         __syncwarp();
         kr.step(p.k_stages);
+        ++k_loads;
       }
       for (int b = KeyPairs::first_block(g, w.q, w.pair); b < w.q.nblk && healthy; ++b) {
         healthy = wait_warp(&qempty[qr.st], qr.ph ^ 1u);
@@ -195,7 +197,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         qr.step(p.q_stages);
+        ++q_loads;
       }
+    }
+    if (!healthy) {
+      await_copies(kfull, p.k_stages, k_loads);
+      await_copies(qfull, p.q_stages, q_loads);
     }
   } else if (warp == 9) {
     // ===================== MMA issue =====================
