@@ -566,7 +566,7 @@ CSA_API size_t gqa_dense_workspace_size(int64_t max_q, int32_t H, int32_t H_kv, 
  *   v   bf16 [total_tokens, H_kv, d_v]
  *   out bf16 [total_tokens, H, d_v];  lse fp32 [total_tokens, H] (nullable)
  *   packed: cu_tokens, n_seqs, max_tokens and total_tokens are used (the entry
- *   offsets are not).  scale > 0 and finite.  Rows of out and lse behind the
+ *   offsets are not).  2^-100 <= scale <= 2^100.  Rows of out and lse behind the
  *   last sequence are left as they were.  A sequence's own keys and values
  *   must be finite; what another sequence holds never reaches it.
  */

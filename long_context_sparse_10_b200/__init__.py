@@ -573,11 +573,12 @@ def gqa_dense_packed(q, k, v, packed: Packed, scale, *, out=None, lse=None, work
     qp = _tensor(q, "q", torch.bfloat16, (packed.total_tokens, H, d_qk), dev)
     kp = _tensor(k, "k", torch.bfloat16, (R, H_kv, d_qk), dev)
     vp = _tensor(v, "v", torch.bfloat16, (R, H_kv, d_v), dev)
-    if packed.cu_tokens.device != dev:
-        raise ValueError(f"the packed offsets are on {packed.cu_tokens.device}, not on {dev}")
+    n = len(packed.lengths)
+    cu = _tensor(packed.cu_tokens, "the packed offsets", torch.int32, (n + 1,), dev)
+    pd = _lib.PackedDesc(cu, None, n, packed.max_tokens, packed.total_tokens, 0)  # the entry offsets are not used
     out, lse, workspace, op, lp, wp, size = _gqa_buffers(lib, q, (R, H, d_qk), d_v, packed.max_tokens, H_kv, out, lse,
                                                          workspace)
-    _check(lib.gqa_dense_packed(qp, kp, vp, ctypes.byref(packed.desc()), H, H_kv, d_qk, d_v, scale, op, lp, wp, size,
+    _check(lib.gqa_dense_packed(qp, kp, vp, ctypes.byref(pd), H, H_kv, d_qk, d_v, scale, op, lp, wp, size,
                                 _current_stream(dev)), "gqa_dense_packed")
     return out, lse
 

@@ -38,7 +38,8 @@ inline csa_status check_heads(const char* what, int32_t H, int32_t H_kv, int32_t
 }
 
 inline csa_status check_scale(const char* what, float scale) {
-  CSA_REQUIRE(std::isfinite(scale) && scale > 0.f, "%s: scale must be positive and finite", what);
+  // far inside what keeps scale * log2(e) and 8 / scale finite
+  CSA_REQUIRE(scale >= 0x1p-100f && scale <= 0x1p100f, "%s: scale must be in [2^-100, 2^100]", what);
   return CSA_OK;
 }
 

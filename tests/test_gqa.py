@@ -63,6 +63,8 @@ def test_struct_layouts():
     (dict(scale=-1.0), INV, b"scale"),
     (dict(scale=math.nan), INV, b"scale"),
     (dict(scale=math.inf), INV, b"scale"),
+    (dict(scale=1e-31), INV, b"scale"),
+    (dict(scale=2e30), INV, b"scale"),
     (dict(c=cache(d_qk=96)), UNS, b"channel widths"),
     (dict(c=cache(d_qk=192, d_v=192)), UNS, b"channel widths"),
     (dict(c=cache(page_size=8)), INV, b"page_size"),
