@@ -4,7 +4,8 @@ Tolerances, per element:
   * out: each probability is rounded to bf16 (half a step, 2^-8 relative) and so is the result: at most
     2^-8 (sum p |v| + |out|), to which the products of both and fp32 arithmetic add less than 2 %;
   * scores: a dot product of d terms in fp32 is off by at most d 2^-23 sum |q c| (truncating accumulation), so lse and
-    the logarithm of a weight by that plus 2^-19 (exp2, log2 and the sums, all in fp32).
+    the logarithm of a weight by that plus 2^-18: exponentials off by at most 2.7e-6 = 2^-18.5 (the polynomial's bound;
+    the unit's is 2^-22), log2 and the sums in fp32 with what is left.
 """
 import math
 
@@ -30,7 +31,7 @@ def f64(t):
 
 
 def score_tol(d, size):
-    return (d + 8) * 2.0**-23 * size + 2.0**-19
+    return (d + 8) * 2.0**-23 * size + 2.0**-18
 
 
 def check_out(got, ref, size, what):
