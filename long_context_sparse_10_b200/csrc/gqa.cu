@@ -113,48 +113,6 @@ constexpr int kMetaOwner = 1;   // the first piece ends its item and does not be
 constexpr int kMetaBegins = 2;  // the last piece begins its item
 constexpr int kMetaSingle = 4;  // the last piece is the first
 
-// (a0, a1) + (b, b) and (a0, a1) * (b0, b1) + (c, c), as above.
-__device__ __forceinline__ void add2s(float& d0, float& d1, float a0, float a1, float b) {
-  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %4};\nadd.rn.f32x2 d, a, b;\n"
-      "mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b));
-}
-__device__ __forceinline__ void sub2(float& d0, float& d1, float a0, float a1) {  // d - a
-  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %4};\nmov.b64 d, {%0, %1};\n"
-      "fma.rn.f32x2 d, a, b, d;\nmov.b64 {%0, %1}, d;\n}\n"
-      : "+f"(d0), "+f"(d1)
-      : "f"(a0), "f"(a1), "f"(-1.f));
-}
-__device__ __forceinline__ void mul_add2(float& d0, float& d1, float b0, float b1, float c) {  // d * b + c
-  asm("{\n.reg .b64 b, c, d;\nmov.b64 b, {%2, %3};\nmov.b64 c, {%4, %4};\nmov.b64 d, {%0, %1};\n"
-      "fma.rn.f32x2 d, d, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
-      : "+f"(d0), "+f"(d1)
-      : "f"(b0), "f"(b1), "f"(c));
-}
-
-// 2^x of two numbers on the fp32 units.  x = n + f with n the nearest whole
-// number (adding 1.5 * 2^23 leaves it in the low bits of the sum) and |f| <= 1/2;
-// 2^f by its minimax polynomial of degree 4 in relative error (fitted by
-// iteratively reweighted least squares; 2.7e-6 off at most in fp32), and n is
-// added to the exponent.  Below 2^-126 the result stays there.
-__device__ __forceinline__ void exp2_fma2(float& x0, float& x1) {
-  constexpr float kMagic = 12582912.f;
-  x0 = fmaxf(x0, -126.f);
-  x1 = fmaxf(x1, -126.f);
-  float t0, t1, n0, n1;
-  add2s(t0, t1, x0, x1, kMagic);
-  add2s(n0, n1, t0, t1, -kMagic);
-  sub2(x0, x1, n0, n1);
-  float y0, y1;
-  fma2(y0, y1, x0, x1, 0.009570102207362652f, 0.05591785907745361f);
-  mul_add2(y0, y1, x0, x1, 0.240247443318367f);
-  mul_add2(y0, y1, x0, x1, 0.6931217908859253f);
-  mul_add2(y0, y1, x0, x1, 0.9999992847442627f);
-  x0 = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23));
-  x1 = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23));
-}
-
 // Probabilities 2^(v * a + b) of a row's 64 scores: written as bf16 pairs to
 // 32 TMEM columns; returns their sum (of the unrounded values).  The
 // exponential unit gives a warp one result in 8 clocks, 2048 for two rows of 128

@@ -88,6 +88,55 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "f"(a0), "f"(a1));
 }
 
+// (a0, a1) + (b, b) and (a0, a1) * (b0, b1) + (c, c), as above.
+__device__ __forceinline__ void add2s(float& d0, float& d1, float a0, float a1, float b) {
+  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %4};\nadd.rn.f32x2 d, a, b;\n"
+      "mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b));
+}
+__device__ __forceinline__ void sub2(float& d0, float& d1, float a0, float a1) {  // d - a
+  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %4};\nmov.b64 d, {%0, %1};\n"
+      "fma.rn.f32x2 d, a, b, d;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1), "f"(-1.f));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmul.rn.f32x2 d, a, b;\n"
+      "mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void mul_add2(float& d0, float& d1, float b0, float b1, float c) {  // d * b + c
+  asm("{\n.reg .b64 b, c, d;\nmov.b64 b, {%2, %3};\nmov.b64 c, {%4, %4};\nmov.b64 d, {%0, %1};\n"
+      "fma.rn.f32x2 d, d, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+      : "+f"(d0), "+f"(d1)
+      : "f"(b0), "f"(b1), "f"(c));
+}
+
+// 2^x of two numbers on the fp32 units.  x = n + f with n the nearest whole
+// number (adding 1.5 * 2^23 leaves it in the low bits of the sum) and |f| <= 1/2;
+// 2^f by its minimax polynomial of degree 4 in relative error (fitted by
+// iteratively reweighted least squares; 2.7e-6 off at most in fp32), and n is
+// multiplied in as a power of two built from those low bits.  Below 2^-126 the
+// result stays there; NaN stays NaN.
+__device__ __forceinline__ void exp2_fma2(float& x0, float& x1) {
+  constexpr float kMagic = 12582912.f;
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x1) : "f"(-126.f));
+  float t0, t1, n0, n1;
+  add2s(t0, t1, x0, x1, kMagic);
+  add2s(n0, n1, t0, t1, -kMagic);
+  sub2(x0, x1, n0, n1);
+  float y0, y1;
+  fma2(y0, y1, x0, x1, 0.009570102207362652f, 0.05591785907745361f);
+  mul_add2(y0, y1, x0, x1, 0.240247443318367f);
+  mul_add2(y0, y1, x0, x1, 0.6931217908859253f);
+  mul_add2(y0, y1, x0, x1, 0.9999992847442627f);
+  mul2(x0, x1, y0, y1, __uint_as_float((__float_as_uint(t0) << 23) + 0x3f800000u),
+       __uint_as_float((__float_as_uint(t1) << 23) + 0x3f800000u));
+}
+
 // Wait of a converged warp for a barrier's phase.  Almost always the phase is there or arrives within one try: that
 // path has one try and a vote, so that no branch of it diverges (a loop whose exit is each lane's own costs 150
 // clocks more).  The bounded loop is for the rest; false, for all lanes, when it runs out.
@@ -139,6 +188,17 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 // Fetches a tensor map (a kernel parameter) ahead of its first use.
 __device__ __forceinline__ void prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
+}
+
+// Whether `x` holds in any of the `threads` threads of barrier `id`.
+__device__ __forceinline__ bool vote(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\nbar.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
 }
 
 // One lane of a converged warp (always the same one).

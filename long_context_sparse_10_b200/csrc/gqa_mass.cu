@@ -281,11 +281,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; b < w.q.nblk; ++b) {
         const int buf = blocks & 1;
         cst[buf * kTile + r] = cur;
+        const int nc = min(g.tpb, w.q.nq - b * g.tpb) * g.G;      // columns that are rows
+        // a row that saw nothing needs an exact 0, which only the exponential unit gives
+        const bool exact = vote(1 + t, kTile, r < nc && cur == -INFINITY);
         cur = constant(b + 1);
-        named_sync(1 + t, kTile);
         if (!wait_warp(&sfull[2 * t + buf], (blocks >> 1) & 1u, limit)) limit = 1;
         tc::fence_after_sync();
-        const int nc = min(g.tpb, w.q.nq - b * g.tpb) * g.G;      // columns that are rows
         const int from = max(key - off - b * g.tpb, 0) * g.G;     // the first that sees the key
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll 1
@@ -302,12 +303,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* e = v + 4 * i;
             fma2v(e[0], e[1], sl2, k.x, k.y);
             fma2v(e[2], e[3], sl2, k.z, k.w);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) e[u] = exp2_approx(e[u]);
           }
-          if (part) {
+          if (part || exact) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = (c + i >= from && c + i < nc) ? v[i] : 0.f;
+            for (int i = 0; i < 32; ++i) v[i] = (c + i >= from && c + i < nc) ? exp2_approx(v[i]) : 0.f;
+          } else {
+            // two of eight pairs on the fp32 units: the exponential unit is the bound where rows are many
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (i % 8 >= 6) {
+                exp2_fma2(v[2 * i], v[2 * i + 1]);
+              } else {
+                v[2 * i] = exp2_in_order(v[2 * i]);
+                v[2 * i + 1] = exp2_in_order(v[2 * i + 1]);
+              }
+            }
           }
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {

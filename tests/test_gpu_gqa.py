@@ -207,6 +207,24 @@ def test_logits_that_grow_move_the_softmax_reference(n):
     c.check(out, lse)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_key_that_is_not_finite_shows_in_the_rows_that_see_it_and_in_no_other(value):
+    L, g = 420, np.random.default_rng(13)
+    for j in list(range(64, 97)) + [0, 127, 128, 255, 300]:
+        q, k, v = bf16(g, L, 2, 128), bf16(g, L, 1, 128), bf16(g, L, 1, 128)
+        q[:, :, 0] = q[:, :, 0].abs() + 0.5  # +inf * q_0 = +inf
+        k[j, 0, 0] = value
+        scale = 0.09
+        out, lse = csa.gqa_dense_packed(q.to(DEV), k.to(DEV), v.to(DEV), csa.Packed([L], 1), scale)
+        out, lse = out.float().cpu(), lse.cpu()
+        assert torch.all(torch.isfinite(out[:j])) and torch.all(torch.isfinite(lse[:j])), j
+        assert torch.all(torch.isnan(out[j:])) and torch.all(torch.isnan(lse[j:])), j
+        if j in (70, 300):
+            ref, rl, size = R.attend(f64(q[:j]), f64(k[:j]), f64(v[:j]), scale, 0)
+            check_out(out[:j].double().numpy(), ref, size, f"key {j}")
+    no_device_error()
+
+
 def test_one_long_sequence_is_shared_by_every_sm():
     c = Case(5, [20011], [1], 1, 8, (128, 128), 128)
     out, lse = csa.gqa_dense_paged(c.q.to(DEV), c.cache, c.batch, c.scale)
