@@ -68,49 +68,6 @@ struct Ring {
   }
 };
 
-struct MassWalk {
-  Seq q;
-  int s, h, pair, count, left;
-
-  __device__ __forceinline__ int cost(const Geometry& g) const {
-    return kItemCost + q.nblk - KeyPairs::first_block(g, q, pair);
-  }
-  // an item belongs to the CTA in whose share its first unit lies
-  __device__ __forceinline__ bool begin(const Geometry& g, const Share& sh) {
-    left = sh.left;
-    if (left <= 0) return false;
-    s = sh.s;
-    h = sh.h;
-    pair = sh.blk;
-    q.load(g, s);
-    count = KeyPairs::count(q);
-    if (sh.unit == 0) return true;
-    left += sh.unit;
-    return next(g);
-  }
-  __device__ __forceinline__ bool next(const Geometry& g) {
-    left -= cost(g);
-    if (left <= 0) return false;
-    if (++pair >= count) {
-      pair = 0;
-      if (++h >= g.Hkv) {
-        h = 0;
-        do {
-          if (++s >= g.n_seqs) return false;
-          q.load(g, s);
-          count = KeyPairs::count(q);
-        } while (count == 0);
-      }
-    }
-    return true;
-  }
-  // whether block b has a row that sees key tile 2 * pair + t
-  __device__ __forceinline__ bool active(const Geometry& g, int t, int b) const {
-    const int k0 = (2 * pair + t) * kTile, last = min((b + 1) * g.tpb, q.nq) - 1;
-    return k0 < q.L && q.L - q.nq + last >= k0;
-  }
-};
-
 template <int DQK>
 __global__ void __launch_bounds__(kThreads, 1)
     gqa_mass_kernel(const __grid_constant__ MassParams p, const __grid_constant__ CUtensorMap qmap,

@@ -24,6 +24,17 @@
 namespace csa {
 namespace gqa {
 
+// The partition's arithmetic runs on the host too, where a test walks it at sizes that no GPU run reaches.
+#define CSA_HD __host__ __device__ __forceinline__
+
+CSA_HD int32_t load_word(const int32_t* p) {
+#ifdef __CUDA_ARCH__
+  return __ldg(p);
+#else
+  return *p;
+#endif
+}
+
 constexpr int kTile = 128;  // keys per tile, and rows per tile
 constexpr int kItemCost = 2;
 
@@ -41,7 +52,7 @@ struct Geometry {
 // sum_{t < n} floor((a t + b) / m) for a n + b < 2^32, in O(log) steps: whole
 // parts come out, and what is left is the same sum with the roles of the axes
 // exchanged (lattice points under the line).
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+CSA_HD int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t ans = 0;
   while (n > 0) {
     if (a >= m) {
@@ -71,27 +82,27 @@ struct Seq {
   int row0;  // first packed row
   int nq, L, nblk;
 
-  __device__ __forceinline__ void load(const Geometry& g, int s) {
-    int64_t a = __ldg(g.cu_q + s), b = __ldg(g.cu_q + s + 1);
+  CSA_HD void load(const Geometry& g, int s) {
+    int64_t a = load_word(g.cu_q + s), b = load_word(g.cu_q + s + 1);
     a = a < 0 ? 0 : (a > g.total_q ? g.total_q : a);
     b = b < a ? a : (b > g.total_q ? g.total_q : b);
     row0 = static_cast<int>(a);
     nq = static_cast<int>(b - a);
     L = nq;
     if (g.cache_len != nullptr) {
-      L = __ldg(g.cache_len + s);
+      L = load_word(g.cache_len + s);
       L = L < 0 ? 0 : (L > g.max_len ? g.max_len : L);
     }
     nblk = (nq + g.tpb - 1) / g.tpb;
   }
   // key tiles of block blk (at least one, so that rows without a key are written too)
-  __device__ __forceinline__ int tiles(const Geometry& g, int blk) const {
+  CSA_HD int tiles(const Geometry& g, int blk) const {
     const int last = min((blk + 1) * g.tpb, nq);
     const int e = L - nq + last;  // keys its last row sees
     return e <= kTile ? 1 : (e + kTile - 1) / kTile;
   }
   // tiles of blocks 0 .. n-1
-  __device__ __forceinline__ int64_t tiles_before(const Geometry& g, int n) const {
+  CSA_HD int64_t tiles_before(const Geometry& g, int n) const {
     int64_t sum = 0;
     if (n == nblk && n > 0) {
       sum = tiles(g, n - 1);
@@ -118,8 +129,8 @@ struct Share {
 
 // The attention's items of a sequence: its row blocks.
 struct Blocks {
-  static __device__ __forceinline__ int count(const Seq& q) { return q.nblk; }
-  static __device__ __forceinline__ int64_t units_before(const Geometry& g, const Seq& q, int n) {
+  static CSA_HD int count(const Seq& q) { return q.nblk; }
+  static CSA_HD int64_t units_before(const Geometry& g, const Seq& q, int n) {
     return q.tiles_before(g, n) + static_cast<int64_t>(n) * kItemCost;
   }
 };
@@ -127,12 +138,12 @@ struct Blocks {
 // The accumulated weight's items: pairs of key tiles, each worth kItemCost and
 // the row blocks (of tpb = tpt tokens) with a row that sees the pair's first key.
 struct KeyPairs {
-  static __device__ __forceinline__ int count(const Seq& q) { return q.nq > 0 ? (q.L + 2 * kTile - 1) / (2 * kTile) : 0; }
-  static __device__ __forceinline__ int first_block(const Geometry& g, const Seq& q, int pair) {
+  static CSA_HD int count(const Seq& q) { return q.nq > 0 ? (q.L + 2 * kTile - 1) / (2 * kTile) : 0; }
+  static CSA_HD int first_block(const Geometry& g, const Seq& q, int pair) {
     const int t = pair * 2 * kTile - (q.L - q.nq);  // the first row that sees the key
     return t <= 0 ? 0 : t / g.tpb;
   }
-  static __device__ __forceinline__ int64_t units_before(const Geometry& g, const Seq& q, int n) {
+  static CSA_HD int64_t units_before(const Geometry& g, const Seq& q, int n) {
     const int off = q.L - q.nq;
     int z = off < 0 ? 0 : off / (2 * kTile) + 1;  // pairs that every block sees
     z = z < n ? z : n;
@@ -143,6 +154,19 @@ struct KeyPairs {
     return units;
   }
 };
+
+// CTA cta's run of `total` units over ctas CTAs (the first ones take one more): its length, and where it begins.
+CSA_HD int64_t share_range(int64_t total, int ctas, int cta, int* left) {
+  const int64_t per = total / ctas, more = total - per * ctas;
+  *left = static_cast<int>(per + (cta < more ? 1 : 0));
+  return per * cta + (cta < more ? cta : more);
+}
+
+// The kv head of unit `at` of a sequence whose heads have `seq` units each: in 32 bits where both fit (a 64-bit
+// division is a subroutine); 1,500,000 tokens with 128 heads on one kv head are 2^32 units.
+CSA_HD int head_of(int64_t at, int64_t seq) {
+  return static_cast<int>(((at | seq) >> 32) ? at / seq : static_cast<uint32_t>(at) / static_cast<uint32_t>(seq));
+}
 
 // All threads of the block call this (blockDim.x a multiple of 32, at most
 // 1024); `scratch` holds 40 int64 words.
@@ -175,9 +199,7 @@ __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ct
   const int ctas = static_cast<int>(total < n_ctas ? total : n_ctas);
   Share sh = {0, 0, 0, 0, 0};
   if (cta >= ctas) return sh;  // the same for every thread of the block
-  const int64_t per = total / ctas, more = total - per * ctas;  // the first `more` CTAs take one unit more
-  const int64_t start = per * cta + (cta < more ? cta : more);
-  sh.left = static_cast<int>(per + (cta < more ? 1 : 0));
+  const int64_t start = share_range(total, ctas, cta, &sh.left);
   if (start >= before && start < before + mine) {
     int64_t at = start - before;
     int s = s0;
@@ -189,7 +211,7 @@ __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ct
       q.load(g, ++s);
       seq = Items::units_before(g, q, Items::count(q));
     }
-    const int h = static_cast<int>((at >> 32) ? at / seq : static_cast<uint32_t>(at) / static_cast<uint32_t>(seq));
+    const int h = head_of(at, seq);
     at -= h * seq;
     scratch[34] = at;
     int32_t* out = reinterpret_cast<int32_t*>(scratch + 32);
@@ -233,7 +255,7 @@ struct Walk {
   bool one;       // the block's rows fit one 128-row tile
 
   // the piece from unit u of the current item; false where it has no tile
-  __device__ __forceinline__ bool set(const Geometry& g, int u) {
+  CSA_HD bool set(const Geometry& g, int u) {
     n = q.tiles(g, blk);
     const int end = min(kItemCost + n, u + left);
     left -= end - u;
@@ -242,7 +264,7 @@ struct Walk {
     one = g.tpb <= g.tpt || q.nq - blk * g.tpb <= g.tpt;
     return t1 > t0;
   }
-  __device__ __forceinline__ bool begin(const Geometry& g, const Share& sh) {
+  CSA_HD bool begin(const Geometry& g, const Share& sh) {
     left = sh.left;
     if (left <= 0) return false;
     s = sh.s;
@@ -251,7 +273,7 @@ struct Walk {
     q.load(g, s);
     return set(g, sh.unit) || next(g);
   }
-  __device__ __forceinline__ bool next(const Geometry& g) {
+  CSA_HD bool next(const Geometry& g) {
     if (left <= 0) return false;
     if (++blk >= q.nblk) {
       blk = 0;
@@ -265,7 +287,51 @@ struct Walk {
     }
     return set(g, 0);  // without a tile only where the share ends in the item's cost
   }
-  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == n; }
+  CSA_HD bool whole() const { return t0 == 0 && t1 == n; }
+};
+
+// Walks a share of key pairs.
+struct MassWalk {
+  Seq q;
+  int s, h, pair, count, left;
+
+  CSA_HD int cost(const Geometry& g) const {
+    return kItemCost + q.nblk - KeyPairs::first_block(g, q, pair);
+  }
+  // an item belongs to the CTA in whose share its first unit lies
+  CSA_HD bool begin(const Geometry& g, const Share& sh) {
+    left = sh.left;
+    if (left <= 0) return false;
+    s = sh.s;
+    h = sh.h;
+    pair = sh.blk;
+    q.load(g, s);
+    count = KeyPairs::count(q);
+    if (sh.unit == 0) return true;
+    left += sh.unit;
+    return next(g);
+  }
+  CSA_HD bool next(const Geometry& g) {
+    left -= cost(g);
+    if (left <= 0) return false;
+    if (++pair >= count) {
+      pair = 0;
+      if (++h >= g.Hkv) {
+        h = 0;
+        do {
+          if (++s >= g.n_seqs) return false;
+          q.load(g, s);
+          count = KeyPairs::count(q);
+        } while (count == 0);
+      }
+    }
+    return true;
+  }
+  // whether block b has a row that sees key tile 2 * pair + t
+  CSA_HD bool active(const Geometry& g, int t, int b) const {
+    const int k0 = (2 * pair + t) * kTile, last = min((b + 1) * g.tpb, q.nq) - 1;
+    return k0 < q.L && q.L - q.nq + last >= k0;
+  }
 };
 
 }  // namespace gqa
