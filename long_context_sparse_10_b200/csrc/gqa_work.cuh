@@ -124,7 +124,8 @@ struct Seq {
 // What one CTA does: `left` units of the list, beginning at unit `unit` of an
 // item.
 struct Share {
-  int left, s, h, blk, unit;
+  int64_t left;  // 2^31 and more for a prompt of 150 million tokens
+  int s, h, blk, unit;
 };
 
 // The attention's items of a sequence: its row blocks.
@@ -156,9 +157,9 @@ struct KeyPairs {
 };
 
 // CTA cta's run of `total` units over ctas CTAs (the first ones take one more): its length, and where it begins.
-CSA_HD int64_t share_range(int64_t total, int ctas, int cta, int* left) {
+CSA_HD int64_t share_range(int64_t total, int ctas, int cta, int64_t* left) {
   const int64_t per = total / ctas, more = total - per * ctas;
-  *left = static_cast<int>(per + (cta < more ? 1 : 0));
+  *left = per + (cta < more ? 1 : 0);
   return per * cta + (cta < more ? cta : more);
 }
 
@@ -251,13 +252,13 @@ struct Walk {
   Seq q;
   int s, h, blk;
   int t0, t1, n;  // this piece's key tiles [t0, t1) of the item's n
-  int left;       // units of the share behind this piece
+  int64_t left;   // units of the share behind this piece
   bool one;       // the block's rows fit one 128-row tile
 
   // the piece from unit u of the current item; false where it has no tile
   CSA_HD bool set(const Geometry& g, int u) {
     n = q.tiles(g, blk);
-    const int end = min(kItemCost + n, u + left);
+    const int end = left < kItemCost + n - u ? u + static_cast<int>(left) : kItemCost + n;
     left -= end - u;
     t0 = max(u - kItemCost, 0);
     t1 = max(end - kItemCost, 0);
@@ -293,7 +294,8 @@ struct Walk {
 // Walks a share of key pairs.
 struct MassWalk {
   Seq q;
-  int s, h, pair, count, left;
+  int64_t left;
+  int s, h, pair, count;
 
   CSA_HD int cost(const Geometry& g) const {
     return kItemCost + q.nblk - KeyPairs::first_block(g, q, pair);

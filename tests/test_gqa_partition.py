@@ -51,6 +51,10 @@ def test_ordinary_batches(walk, op, Hkv, G, n, lens):
     ("attention", 1, 64, 2_100_000, 2_100_000, 1 << 32),
     ("weight", 1, 128, 1_500_000, 1_500_000, 1 << 32),
     ("weight", 3, 100, 1_500_000, 1_500_000, 1 << 32),
+    # one CTA's share counts 2^31 units and more
+    ("attention", 1, 1, 300_000_000, 300_000_000, 148 << 31),
+    ("attention", 1, 16, 40_000_000, 40_000_000, 148 << 31),
+    ("weight", 1, 1, 300_000_000, 300_000_000, 148 << 31),
 ])
 def test_counts_beyond_32_bits(walk, op, Hkv, G, n, L, units):
     assert walk(op, Hkv, G, [n], [L]) >= units
