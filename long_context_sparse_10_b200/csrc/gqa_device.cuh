@@ -190,17 +190,6 @@ __device__ __forceinline__ void prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }
 
-// Whether `x` holds in any of the `threads` threads of barrier `id`.
-__device__ __forceinline__ bool vote(int id, int threads, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %3, 0;\nbar.red.or.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x))
-      : "memory");
-  return r != 0;
-}
-
 // One lane of a converged warp (always the same one).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;

@@ -239,8 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int buf = blocks & 1;
         cst[buf * kTile + r] = cur;
         const int nc = min(g.tpb, w.q.nq - b * g.tpb) * g.G;      // columns that are rows
-        // a row that saw nothing needs an exact 0, which only the exponential unit gives
-        const bool exact = vote(1 + t, kTile, r < nc && cur == -INFINITY);
+        named_sync(1 + t, kTile);
         cur = constant(b + 1);
         if (!wait_warp(&sfull[2 * t + buf], (blocks >> 1) & 1u, limit)) limit = 1;
         tc::fence_after_sync();
@@ -261,20 +260,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             fma2v(e[0], e[1], sl2, k.x, k.y);
             fma2v(e[2], e[3], sl2, k.z, k.w);
           }
-          if (part || exact) {
+          // all on the exponential unit: the weight is summed over a sequence's life, lse is the caller's (nothing bounds
+          // the exponent), and two of eight pairs on the fp32 units gain nothing (64 rows of four sequences 20.6 us, both)
+          if (part) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = (c + i >= from && c + i < nc) ? exp2_approx(v[i]) : 0.f;
           } else {
-            // two of eight pairs on the fp32 units: the exponential unit is the bound where rows are many
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (i % 8 >= 6) {
-                exp2_fma2(v[2 * i], v[2 * i + 1]);
-              } else {
-                v[2 * i] = exp2_in_order(v[2 * i]);
-                v[2 * i + 1] = exp2_in_order(v[2 * i + 1]);
-              }
-            }
+            for (int i = 0; i < 32; ++i) v[i] = exp2_approx(v[i]);
           }
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {

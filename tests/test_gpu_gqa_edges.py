@@ -1,0 +1,90 @@
+"""Accumulated weight and grouped-head attention where their arithmetic can go wrong: large weights, single exponentials
+to the exponential unit's accuracy.
+
+ex2.approx is off by at most 2^-22 relative; a product or sum in fp32 by 2^-24, a constant rounded to fp32 likewise."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import long_context_sparse_10_b200 as csa
+from oracle import gqa_ref as R
+from test_gpu_gqa import DEV, DIMS, Case, f64, i32, no_device_error
+
+pytestmark = pytest.mark.gpu
+
+
+def one_channel(values, d):
+    """Keys or queries [..., d] whose channel 0 holds the values: their products are exact."""
+    t = torch.zeros(*values.shape, d)
+    t[..., 0] = values
+    return t.to(torch.bfloat16)
+
+
+def close_or_infinite(got, want, tol):
+    """The worst relative error of what fp32 holds; what it does not hold has to be +inf."""
+    top = float(np.finfo(np.float32).max)
+    assert bool(np.all(np.isposinf(got[want > top * (1 + tol)])))
+    held = want < top * (1 - tol)
+    worst = float(np.abs(got[held] / want[held] - 1).max()) if held.any() else 0.0
+    assert worst <= tol, f"{worst:.3e}, {tol:.3e} allowed"
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("lse", [-60.0, -86.0, -95.0, -200.0, -1e30])
+def test_weights_of_an_lse_far_below_the_scores(dims, lse):
+    # an lse that is not the rows' own: weights of e^(score - lse), which leave fp32 above e^88.7
+    n, G, L, page = 32, 4, 300, 32
+    c = Case(5, [L], [n], 1, G, dims, page)
+    c.cache.k.zero_()
+    c.cache.mass.zero_()
+    q = torch.zeros(n, G, dims[0], dtype=torch.bfloat16, device=DEV)
+    got = csa.gqa_cache_mass(q, torch.full((n, G), lse, device=DEV), c.cache, c.batch, 1.0)
+    no_device_error()
+    rows = np.array([min(n, L - j) for j in range(L)]) * G
+    # the exponent -lse log2(e) is rounded (twice 2^-24 of up to 124.1, in units of ln 2), the unit 2^-22, 128 sums
+    tol = (2 * 124.1 * math.log(2) + 4 + 128) * 2.0**-24
+    close_or_infinite(R.live(f64(got), c.table[0], L)[:, 0], rows * np.exp(min(-lse, 700.0)), tol)
+
+
+@pytest.mark.parametrize("lse", [-60.0, -86.0, -95.0, -178.0, -200.0, -1e30])
+def test_one_weight_of_an_lse_far_below_the_scores(lse):
+    # of 64 rows, one row of each 16 in turn; the others weigh e^-80
+    n, L, page, d = 64, 200, 16, 64
+    pages = -(-L // page)
+    q = torch.zeros(n, 1, d, dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros(pages, 1, page, d, dtype=torch.bfloat16, device=DEV)
+    batch = csa.GqaBatch(i32(np.arange(pages)[None]), i32([L]), i32([0, n]), max_q=n, total_q=n)
+    tol = (2 * 124.1 * math.log(2) + 4 + 2) * 2.0**-24
+    for row in range(16):
+        mass = torch.zeros(pages, 1, page, device=DEV)
+        at = torch.full((n, 1), 80.0, device=DEV)
+        at[row] = lse
+        csa.gqa_cache_mass(q, at, csa.GqaCache(k, k, mass), batch, 1.0)
+        close_or_infinite(f64(mass).reshape(-1)[: L - n], np.full(L - n, np.exp(min(-lse, 700.0))), tol)
+    no_device_error()
+
+
+def test_a_weight_is_as_exact_as_the_exponential_unit():
+    # 64 rows of one head; all but one weigh e^-80.  Every column of a 16-column run in turn, exponents in [-1, 1].
+    n, L, page, d = 64, 200, 16, 128
+    g = np.random.default_rng(3)
+    x = torch.from_numpy(g.uniform(-1, 1, L).astype(np.float32)).to(torch.bfloat16).float()
+    pages = -(-L // page)
+    k = torch.zeros(pages, 1, page, d, dtype=torch.bfloat16)
+    k.view(-1, d)[:L] = one_channel(x, d)
+    v = torch.zeros_like(k)
+    q = one_channel(torch.ones(n, 1), d).to(DEV)
+    # exponent: scale log2(e) rounded (2 2^-24 relative, |x| <= 1), the fused product and sum 2^-24; the unit; the sum
+    tol = (3 * math.log(2) + 4 + 2) * 2.0**-24
+    for row in range(16):
+        cache = csa.GqaCache(k.to(DEV), v.to(DEV), torch.zeros(pages, 1, page, device=DEV))
+        batch = csa.GqaBatch(i32(np.arange(pages)[None]), i32([L]), i32([0, n]), max_q=n, total_q=n)
+        lse = torch.full((n, 1), 80.0, device=DEV)
+        lse[row] = 0.0
+        got = f64(csa.gqa_cache_mass(q, lse, cache, batch, 1.0)).reshape(-1)[: L - n]
+        want = np.exp(f64(x))[: L - n]
+        worst = float(np.abs(got / want - 1).max())
+        assert worst <= tol, f"row {row}: {worst:.3e}, {tol:.3e} allowed"
+    no_device_error()
