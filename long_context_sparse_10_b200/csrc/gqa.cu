@@ -71,7 +71,6 @@ constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kWgThreads = 128;
 constexpr int kStep = 64;  // keys of half a tile
-constexpr int kFmas = 2;   // of 8 pairs of exponentials, those on the fp32 units
 constexpr float kRescaleLog2 = 8.f;
 
 // SINGLE: every item of the call fits one 128-row tile (decode), so one Q tile
@@ -113,11 +112,17 @@ constexpr int kMetaOwner = 1;   // the first piece ends its item and does not be
 constexpr int kMetaBegins = 2;  // the last piece begins its item
 constexpr int kMetaSingle = 4;  // the last piece is the first
 
+// Pairs of every 8 whose exponentials are computed on the fp32 units.  The exponential unit gives a warp one result in
+// 8 clocks, 2048 for two rows of 128 keys: longer than their MMAs where a key has 64 channels, and only there does it
+// pay (sustained, two pairs against none: 8192-token prompt of 64 channels 464 against 482 us, documents 139 against
+// 142, chunks 204 against 209; of 128 channels 597 and 596; of 192 channels 386 against 365; 4096 tokens, one query
+// head per kv head, 103 against 98; three pairs lose everywhere).  A decode step waits for its K/V stream, and the
+// polynomial is less exact (2.7e-6 against 2^-22): none.
+constexpr int fp32_pairs(int dqk, bool single) { return dqk == 64 && !single ? 2 : 0; }
+
 // Probabilities 2^(v * a + b) of a row's 64 scores: written as bf16 pairs to
-// 32 TMEM columns; returns their sum (of the unrounded values).  The
-// exponential unit gives a warp one result in 8 clocks, 2048 for two rows of 128
-// keys, as long as their MMAs; so FMAS of every 8 pairs are computed on the fp32
-// units instead (8192-token prompt: none 554 us, one 550, two 542, three 610).
+// 32 TMEM columns; returns their sum (of the unrounded values).  FMAS of every
+// 8 pairs are computed on the fp32 units instead of the exponential unit.
 template <int FMAS>
 __device__ __forceinline__ float probabilities(float* v, float a, float b, uint32_t tP) {
   // Sixteen at a time, and while the exponential unit works on these, the sums and roundings of the sixteen before: in
@@ -546,9 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (warp_valid) {
             float v[kStep];
             load_scores(v, tS + hh * kStep, masked, vis - hh * kStep);
+            constexpr int kPairs = fp32_pairs(DQK, SINGLE);
             // a masked tile's -inf needs an exact 0, which only the exponential unit gives
-            l += masked ? probabilities<0>(v, sl2, ref, tS + hh * (kStep / 2))
-                        : probabilities<kFmas>(v, sl2, ref, tS + hh * (kStep / 2));
+            if (kPairs == 0 || masked)
+              l += probabilities<0>(v, sl2, ref, tS + hh * (kStep / 2));
+            else
+              l += probabilities<kPairs>(v, sl2, ref, tS + hh * (kStep / 2));
             tc::tmem_wait_st();
           }
           tc::fence_before_sync();

@@ -88,3 +88,31 @@ def test_a_weight_is_as_exact_as_the_exponential_unit():
         worst = float(np.abs(got / want - 1).max())
         assert worst <= tol, f"row {row}: {worst:.3e}, {tol:.3e} allowed"
     no_device_error()
+
+
+@pytest.mark.parametrize("dims", DIMS)
+def test_lse_of_a_decode_step_is_as_exact_as_the_exponential_unit(dims):
+    # Two keys count: one of score 0 in the first tile, one of score x ln 2, 1 <= x < 2, in the third (the same stream,
+    # and not far enough above to move the reference); the others weigh nothing.  Many copies, so that most items are
+    # one CTA's.
+    L, page, copies, scale = 384, 128, 40, math.log(2)
+    xs = [1 + i / 32 for i in range(32)]
+    score = torch.full((len(xs), L), -5000.0)
+    score[:, 0] = 0.0
+    for i, x in enumerate(xs):
+        score[i, 256 + 12 + i % 4 + 16 * (i % 8)] = x
+    k = one_channel(score.view(len(xs) * 3, 1, page), dims[0])
+    v = torch.zeros(len(xs) * 3, 1, page, dims[1], dtype=torch.bfloat16)
+    n = len(xs) * copies
+    table = np.arange(len(xs) * 3).reshape(-1, 3)[np.arange(n) % len(xs)]
+    cache = csa.GqaCache(k.to(DEV), v.to(DEV))
+    batch = csa.GqaBatch(i32(table), i32([L] * n), i32(range(n + 1)), max_q=1, total_q=n)
+    q = one_channel(torch.ones(n, 1), dims[0]).to(DEV)
+    _, lse = csa.gqa_dense_paged(q, cache, batch, scale)
+    no_device_error()
+    want = np.log1p(np.exp(np.array(xs) * float(np.float32(scale))))[np.arange(n) % len(xs)]
+    # in log2 units and 2^-24: scale log2(e) 2 x; the exponent's rounding x; the unit 4 log2(e); the sum log2(e); log2f
+    # (1 ulp below 4) 4; the result's sum and product with a rounded ln 2, below 2.33, 3 * 2.33: below 2^-19 all in all
+    tol = math.log(2) * (2 * 2 + 2 + 5 * 1.4427 + 4 + 3 * 2.33) * 2.0**-24
+    err = np.abs(f64(lse)[:, 0] - want)
+    assert err.max() <= tol, f"{err.max():.3e}, {tol:.3e} allowed, at x = {xs[int(err.argmax()) % len(xs)]}"
