@@ -567,10 +567,12 @@ CSA_API size_t gqa_dense_workspace_size(int64_t max_q, int32_t H, int32_t H_kv, 
  *   out bf16 [total_tokens, H, d_v];  lse fp32 [total_tokens, H] (nullable)
  *   packed: cu_tokens, n_seqs, max_tokens and total_tokens are used (the entry
  *   offsets are not).  2^-100 <= scale <= 2^100.  Rows of out and lse behind the
- *   last sequence are left as they were.  A key that is not finite shows as NaN
- *   in the rows that see it and in no other.  A sequence's own values must be
- *   finite: one that is not also reaches rows shortly before it (those that
- *   share its tile of 128 keys).  What another sequence holds never reaches it.
+ *   last sequence are left as they were.  A score that is NaN or +inf (of a key
+ *   that is not finite) shows as NaN in the row that sees it and in no other; a
+ *   score of -inf weighs nothing, and a row that sees no other gets out = 0 and
+ *   lse = -inf.  A sequence's own values must be finite: one that is not also
+ *   reaches rows shortly before it (those that share its tile of 128 keys).
+ *   What another sequence holds never reaches it.
  */
 CSA_API csa_status gqa_dense_packed(const void* q, const void* k, const void* v, const csa_packed* packed, int32_t H,
                                     int32_t H_kv, int32_t d_qk, int32_t d_v, float scale, void* out, float* lse,

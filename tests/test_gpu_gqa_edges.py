@@ -10,7 +10,7 @@ import torch
 
 import long_context_sparse_10_b200 as csa
 from oracle import gqa_ref as R
-from test_gpu_gqa import DEV, DIMS, Case, f64, i32, no_device_error
+from test_gpu_gqa import DEV, DIMS, Case, bf16, check_lse, check_out, f64, i32, no_device_error, score_tol
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,51 @@ def test_lse_of_a_decode_step_is_as_exact_as_the_exponential_unit(dims):
     tol = math.log(2) * (2 * 2 + 2 + 5 * 1.4427 + 4 + 3 * 2.33) * 2.0**-24
     err = np.abs(f64(lse)[:, 0] - want)
     assert err.max() <= tol, f"{err.max():.3e}, {tol:.3e} allowed, at x = {xs[int(err.argmax()) % len(xs)]}"
+
+
+@pytest.mark.parametrize("dims", DIMS)
+def test_a_score_of_minus_infinity_weighs_nothing(dims):
+    # keys whose product with every query is -inf, at both ends of tiles and of what a row sees; the rows that see no
+    # other key have out 0 and lse -inf
+    L, G, scale = 420, 2, 0.09
+    bad = [0, 1, 63, 64, 127, 128, 129, 200, 255, 300, 419]
+    g = np.random.default_rng(17)
+    q, k, v = bf16(g, L, G, dims[0]), bf16(g, L, 1, dims[0]), bf16(g, L, 1, dims[1])
+    q[:, :, 0] = q[:, :, 0].abs() + 0.5
+    k[bad, 0, 0] = -math.inf
+    out, lse = csa.gqa_dense_packed(q.to(DEV), k.to(DEV), v.to(DEV), csa.Packed([L], 1), scale)
+    no_device_error()
+    out, lse = f64(out), f64(lse)
+    assert np.all(out[:2] == 0) and np.all(np.isneginf(lse[:2]))
+    good = [j for j in range(L) if j not in bad]
+    kg, vg = f64(k[good]), f64(v[good])
+    for t in range(2, L):
+        m = sum(j <= t for j in good)
+        qs = f64(q[t:t + 1])
+        ref, rl, size = R.attend(qs, kg, vg, scale, m - 1)
+        check_out(out[t:t + 1], ref, size, f"row {t}")
+        check_lse(lse[t:t + 1], rl, score_tol(dims[0], R.score_size(qs, kg[:m], scale)), f"row {t}")
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("value", [float("nan"), math.inf, -math.inf])
+def test_a_key_that_is_not_finite_in_a_long_cache(dims, value):
+    # a decode step whose keys are shared out over many CTAs: the one key shows in the row, or weighs nothing
+    L, G, page = 5000, 4, 64
+    for at in (0, 130, 2500, 4999):
+        c = Case(19, [L], [1], 1, G, dims, page)
+        c.q[:, :, 0] = c.q[:, :, 0].abs() + 0.5
+        c.cache.k[c.table[0, at // page], 0, at % page, 0] = value
+        out, lse = csa.gqa_dense_paged(c.q.to(DEV), c.cache, c.batch, c.scale)
+        before = c.cache.mass.clone()
+        mass = csa.gqa_cache_mass(c.q.to(DEV), lse, c.cache, c.batch, c.scale)
+        no_device_error()
+        if value == -math.inf:
+            ks, vs = np.delete(c.live(c.k, 0), at, 0), np.delete(c.live(c.v, 0), at, 0)
+            ref, rl, size = R.attend(f64(c.q), ks, vs, c.scale, L - 2)
+            check_out(f64(out), ref, size, f"key {at}")
+            check_lse(f64(lse), rl, score_tol(dims[0], R.score_size(f64(c.q), ks, c.scale)), f"key {at}")
+            pg, sl = c.table[0, at // page], at % page
+            assert float(mass[pg, 0, sl]) == float(before[pg, 0, sl])
+        else:
+            assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all()), at
