@@ -164,3 +164,23 @@ def test_a_key_that_is_not_finite_in_a_long_cache(dims, value):
             assert float(mass[pg, 0, sl]) == float(before[pg, 0, sl])
         else:
             assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all()), at
+
+
+def test_items_in_which_a_stream_has_no_tile_against_the_oracle():
+    # decode rows of one key tile give the second stream nothing, and so do chunks whose keys end in their first tile:
+    # the idle stream's accumulator, reference and sum, left by an item before, count for nothing
+    for seed, (L, n) in enumerate(((100, 1), (128, 1), (129, 2), (257, 1), (40, 40), (300, 70))):
+        lens = [max(n, L - i % 7) for i in range(200)]
+        c = Case(60 + seed, lens, [n] * 200, 1, 4, (64, 64), 16)
+        out, lse = csa.gqa_dense_paged(c.q.to(DEV), c.cache, c.batch, c.scale)
+        torch.cuda.synchronize()
+        no_device_error()
+        out, lse = f64(out), f64(lse)
+        for s in range(200):
+            a, b = c.cu[s], c.cu[s + 1]
+            rows = sorted({a, (a + b) // 2, b - 1})  # first, middle and last row of each sequence
+            qs, ks, vs = f64(c.q[a:b]), c.live(c.k, s), c.live(c.v, s)
+            for r in rows:
+                ref, rl, size = R.attend(qs[r - a:r - a + 1], ks, vs, c.scale, lens[s] - (b - a) + r - a)
+                check_out(out[r:r + 1], ref, size, f"{(L, n)} sequence {s}")
+                check_lse(lse[r:r + 1], rl, score_tol(64, R.score_size(qs, ks, c.scale)), f"{(L, n)} sequence {s}")
