@@ -184,3 +184,82 @@ def test_items_in_which_a_stream_has_no_tile_against_the_oracle():
                 ref, rl, size = R.attend(qs[r - a:r - a + 1], ks, vs, c.scale, lens[s] - (b - a) + r - a)
                 check_out(out[r:r + 1], ref, size, f"{(L, n)} sequence {s}")
                 check_lse(lse[r:r + 1], rl, score_tol(64, R.score_size(qs, ks, c.scale)), f"{(L, n)} sequence {s}")
+
+
+def attend64(q, k, v, scale):
+    """Causal attention of one prompt in 64 bits on the device: out, lse, the softmax mean of |v|, and for each row the
+    largest scale * sum |q_c k_c|; a query head at a time."""
+    n, H, _ = q.shape
+    G = H // k.shape[1]
+    hidden = torch.ones(n, n, dtype=torch.bool, device=q.device).triu(1)
+    out, lse, mean, size = [], [], [], 0.0
+    for h in range(H):
+        qh, kh, vh = q[:, h].double(), k[:, h // G].double(), v[:, h // G].double()
+        x = (scale * (qh @ kh.T)).masked_fill(hidden, -math.inf)
+        m = torch.logsumexp(x, 1)
+        p = torch.exp(x - m[:, None])
+        out.append(p @ vh)
+        mean.append(p @ vh.abs())
+        lse.append(m)
+        size = max(size, scale * float((qh.abs() @ kh.abs().T).max()))
+    return torch.stack(out, 1), torch.stack(lse, 1), torch.stack(mean, 1), size
+
+
+@pytest.mark.parametrize("lens,Hkv,G,dims", [
+    ([4001], 2, 1, (128, 128)),
+    ([4001], 1, 4, (192, 128)),
+    ([2600, 1700, 3], 2, 2, (64, 64)),
+    ([1300, 2050], 1, 12, (128, 128)),
+    ([1600], 1, 8, (64, 64)),
+])
+def test_every_row_of_long_prompts_and_their_weight(lens, Hkv, G, dims):
+    """Whole prompts against 64 bits, row by row, and the weight that all their rows give their tokens."""
+    g = np.random.default_rng(sum(lens))
+    page, scale, n = 64, 1 / math.sqrt(dims[0]), sum(lens)
+    q, k, v = (t.to(DEV) for t in (bf16(g, n, Hkv * G, dims[0]), bf16(g, n, Hkv, dims[0]), bf16(g, n, Hkv, dims[1])))
+    out, lse = csa.gqa_dense_packed(q, k, v, csa.Packed(lens, 1), scale)
+    need = [-(-L // page) for L in lens]
+    P = sum(need)
+    order = iter(g.permutation(P))
+    table = np.zeros((len(lens), max(need)), np.int32)
+    for s, c in enumerate(need):
+        table[s, :c] = [next(order) for _ in range(c)]
+    cache = csa.GqaCache(*[torch.full((P, Hkv, page, d), float("nan"), dtype=torch.bfloat16, device=DEV) for d in dims],
+                         torch.full((P, Hkv, page), float("nan"), device=DEV))
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    batch = csa.GqaBatch(i32(table), i32(lens), i32(cu), max_q=max(lens), total_q=n)
+    csa.gqa_cache_append(k, v, cache, batch)
+    mass = csa.gqa_cache_mass(q, lse, cache, batch, scale)
+    again = csa.GqaCache(cache.k, cache.v, torch.zeros_like(mass))
+    csa.gqa_cache_mass(q, lse, again, batch, scale)
+    torch.cuda.synchronize()
+    no_device_error()
+    for s, L in enumerate(lens):
+        a, b = cu[s], cu[s + 1]
+        ref, rl, mean, size = attend64(q[a:b], k[a:b], v[a:b], scale)
+        check_out(f64(out[a:b]), f64(ref), f64(mean), f"sequence {s}")
+        check_lse(f64(lse[a:b]), f64(rl), score_tol(dims[0], size), f"sequence {s}")
+        add = torch.zeros(Hkv, L, dtype=torch.float64, device=DEV)
+        hidden = torch.ones(L, L, dtype=torch.bool, device=DEV).triu(1)
+        for h in range(Hkv * G):  # with the rows' own lse, as the call has it
+            x = scale * (q[a:b, h].double() @ k[a:b, h // G].double().T) - lse[a:b, h].double()[:, None]
+            add[h // G] += torch.exp(x.masked_fill(hidden, -math.inf)).sum(0)
+        got = R.live(f64(mass), table[s], L).T
+        # a weight's relative error and a sum of at most L G of them (four partial sums a block of rows, then the blocks)
+        rel = score_tol(dims[0], size) + (128 // 4 + 4 + L * G // (128 // G * G) + 2) * 2.0**-24
+        worst = float((np.abs(got - f64(add)) / f64(add)).max())
+        assert worst <= rel, f"sequence {s}: {worst:.3e}, {rel:.3e} allowed"
+        assert np.array_equal(R.live(f64(again.mass), table[s], L).T, got)  # the same bits every time
+
+
+@pytest.mark.parametrize("lens,n,Hkv,G,dims", [
+    ([1500, 700, 2049, 130], [4, 2, 8, 3], 2, 8, (128, 128)),   # one tile of rows
+    ([1500, 700, 2049, 130], [8, 5, 8, 1], 1, 32, (64, 64)),    # two
+    ([1200, 640], [5, 6], 2, 1, (192, 128)),
+])
+def test_a_few_new_rows_a_sequence(lens, n, Hkv, G, dims):
+    c = Case(70 + G, lens, n, Hkv, G, dims, 64)
+    out, lse = csa.gqa_dense_paged(c.q.to(DEV), c.cache, c.batch, c.scale)
+    torch.cuda.synchronize()
+    no_device_error()
+    c.check(out, lse)
