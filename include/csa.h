@@ -605,7 +605,10 @@ CSA_API csa_status gqa_cache_append(const void* k, const void* v, const gqa_cach
  * chunk's rows give it, summed over the rows and the G heads of its group:
  *     mass[h, j] += sum_{i: position of row i >= j} sum_{g<G} exp(scale q[i,hG+g] . k[j,h] - lse[i,hG+g])
  * with the lse of gqa_dense_paged for the same rows; a row with lse = -inf
- * adds nothing.  The sum of a call is taken in fp32 in a fixed order.
+ * adds nothing.  A sequence's sum is taken in fp32 in a fixed order and added to
+ * the token in one addition: a token of one sequence gets the same bits every
+ * time.  Where sequences of the call share a page, their additions to its
+ * tokens come in any order, and the last bit may differ from run to run.
  *   q bf16 [total_q, H, d_qk];  lse fp32 [total_q, H];  cache->mass is updated
  */
 CSA_API csa_status gqa_cache_mass(const void* q, const float* lse, const gqa_cache* cache, const gqa_batch* batch,

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_arrive_if(&sempty[2 * t + buf], lane == 0);
         ++blocks;
       }
-      // the only addition of this call to the token, unless sequences share the page
+      // the only addition of this call to the token, unless sequences share the page: theirs come in any order
       if (at >= 0) atomicAdd(p.c.mass + at, sum);
     }
     pdl_trigger();
