@@ -381,7 +381,6 @@ csa_status gqa_cache_evict(const gqa_cache* cache, const gqa_batch* batch, int32
   p.kept = kept;
   p.new_len = new_len;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  prof_begin(s);
   // A cluster per list: enough blocks that each has about 4096 positions of the longest (at 65536 positions and 32
   // lists: 274 us with one block of 1024 threads per list).
   const int longest = batch->max_pages * cache->page_size;
