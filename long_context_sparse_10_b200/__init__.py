@@ -474,6 +474,8 @@ def _elsewhere(device, stream):
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, not on {device}")
         return torch.cuda.stream(stream)
     return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
