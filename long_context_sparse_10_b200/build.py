@@ -6,7 +6,7 @@ Objects go to <repo>/_build/ and the shared library next to this file, so it
 travels with the source tree.  A source is recompiled when it or any header is
 newer than its object.  `--checked` builds libcsa_checked.so (objects in
 _build/checked/) with -DCSA_CHECKED: the kernels bounds-check their gather rows
-and record a failed check in the device error word that
+and slots and record a failed check in the device error word that
 csa_check_device_error reports (load it with CSA_LIBRARY=<path>).
 """
 from __future__ import annotations

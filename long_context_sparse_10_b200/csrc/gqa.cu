@@ -599,6 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;  // NaN stays NaN
         const int64_t grow = static_cast<int64_t>(w.q.row0 + tok) * p.Hq + w.h * g.G + rg;
         const int64_t prow = (static_cast<int64_t>(2) * blockIdx.x + (items > 0 ? 1 : 0)) * S::kRows + s * kTile + r;
+        const bool mine = valid && CSA_INBOUNDS(whole ? grow >= 0 && grow < g.total_q * p.Hq
+                                                      : prow >= 0 && prow < static_cast<int64_t>(2) * gridDim.x * S::kRows);
         fa *= inv;
         fb *= inv;
         const bool any_a = __any_sync(0xffffffffu, valid && fa != 0.f), any_b = __any_sync(0xffffffffu, valid && fb != 0.f);
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] += fb != 0.f ? o2[i] * fb : 0.f;
           }
-          if (valid) {
+          if (mine) {
             if (whole) {
               uint32_t u[8];
 #pragma unroll
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (valid) {
+        if (mine) {
           if (whole) {
             if (p.lse != nullptr) p.lse[grow] = l == 0.f ? -INFINITY : (mr + log2f(l)) * kLn2;
           } else {
@@ -683,8 +685,10 @@ __global__ void __launch_bounds__(256) gqa_merge_kernel(const __grid_constant__ 
     const uint32_t begins = __ballot_sync(0xffffffffu, i > 0 && (from <= 0 || (info.x & kMetaBegins)));
     const int n = begins ? __ffs(begins) : 32;  // pieces here
     const int second = (i > 0 && !(info.x & kMetaSingle)) ? 1 : 0;
-    const int64_t slot = (static_cast<int64_t>(2) * max(from, 0) + second) * ROWS + row;
-    const float2 ml = lane < n ? p.ml[slot] : make_float2(-INFINITY, 0.f);
+    int64_t slot = (static_cast<int64_t>(2) * max(from, 0) + second) * ROWS + row;
+    const bool held = lane < n && CSA_INBOUNDS(from >= 0 && slot < static_cast<int64_t>(2) * gridDim.x * ROWS);
+    if (!held) slot = 0;
+    const float2 ml = held ? p.ml[slot] : make_float2(-INFINITY, 0.f);
     const float now = fmaxf(top, warp_max(ml.x)), ref = now == -INFINITY ? 0.f : now;
     const float old = top == -INFINITY ? 0.f : exp2f(top - ref);
     const float wgt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - ref);
@@ -712,6 +716,7 @@ __global__ void __launch_bounds__(256) gqa_merge_kernel(const __grid_constant__ 
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   const int64_t grow = static_cast<int64_t>(q.row0 + tok) * p.Hq + h * p.g.G + rg;
+  if (!CSA_INBOUNDS(grow >= 0 && grow < p.g.total_q * p.Hq)) return;
   if (lane < DV / 4)
     *reinterpret_cast<uint2*>(p.out + grow * DV + 4 * lane) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));

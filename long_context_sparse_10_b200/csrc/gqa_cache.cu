@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(256) gqa_append_kernel(const __grid_constant__
   const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= p.total_q || row >= __ldg(p.cu_q + p.n_seqs)) return;
   const int s = seq_of(p.cu_q, p.n_seqs, row);
+  if (!CSA_INBOUNDS(s >= 0 && s < p.n_seqs)) return;
   const int end = __ldg(p.cu_q + s + 1);
   const int pos = __ldg(p.cache_len + s) - end + static_cast<int>(row);
   const int64_t at = slot_of(p.c, p.block_table + static_cast<int64_t>(s) * p.max_pages, p.max_pages, 0, pos);
@@ -119,7 +120,8 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
   auto keys4 = [&](int j) -> uint4 { return held ? *reinterpret_cast<const uint4*>(keys + (j - a)) : read4(j); };
   if (held) {
 #pragma unroll 4
-    for (int j = a + 4 * tid; j < b; j += kRun) *reinterpret_cast<uint4*>(keys + (j - a)) = read4(j);
+    for (int j = a + 4 * tid; j < b; j += kRun)
+      if (CSA_INBOUNDS(j >= a && j - a + 4 <= p.held)) *reinterpret_cast<uint4*>(keys + (j - a)) = read4(j);
   }
   uint32_t prefix = 0;
   int need = want;  // of the keys that share the prefix
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(kSelThreads) gqa_evict_select_kernel(const __g
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const bool e = (eq >> u) & 1u, take = ((gt >> u) & 1u) || (e && eq_before < open);
-      if (take && at < p.budget) kept[at] = j + 4 * lane + u;
+      if (take && at < p.budget && CSA_INBOUNDS(at >= 0)) kept[at] = j + 4 * lane + u;
       at += take ? 1 : 0;
       eq_before += e ? 1 : 0;
     }

@@ -212,7 +212,7 @@ __device__ __forceinline__ int64_t slot_of(const Pool& c, const int32_t* table, 
   const int pg = pos >> c.shift;
   if (pos < 0 || pg >= max_pages) return -1;
   const int id = __ldg(table + pg);
-  if (id < 0 || id >= c.n_pages) return -1;
+  if (id < 0 || id >= c.n_pages || !CSA_INBOUNDS(h >= 0 && h < c.Hkv)) return -1;
   return ((static_cast<int64_t>(id) * c.Hkv + h) << c.shift) + (pos & (c.page - 1));
 }
 

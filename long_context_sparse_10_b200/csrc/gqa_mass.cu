@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // -lse of column r in log2 units; rows that are none, or saw nothing, add nothing
       auto constant = [&](int b) {
         const int tok = b * g.tpb + ct;
-        if (b >= w.q.nblk || ct >= g.tpt || tok >= w.q.nq) return -INFINITY;
+        if (b >= w.q.nblk || ct >= g.tpt || tok >= w.q.nq || !CSA_INBOUNDS(tok >= 0 && w.q.row0 + tok < g.total_q))
+          return -INFINITY;
         const float l = __ldg(p.lse + (static_cast<int64_t>(w.q.row0 + tok) * g.Hkv + w.h) * g.G + cg);
         return l == -INFINITY ? -INFINITY : -l * kLog2e;
       };

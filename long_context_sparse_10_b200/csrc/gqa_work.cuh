@@ -244,6 +244,7 @@ __device__ __forceinline__ Share find_share(const Geometry& g, int cta, int n_ct
   sh.h = out[1];
   sh.blk = out[2];
   sh.unit = out[3];
+  if (!CSA_INBOUNDS(sh.s >= 0 && sh.s < g.n_seqs && sh.h >= 0 && sh.h < g.Hkv && sh.blk >= 0 && sh.unit >= 0)) sh.left = 0;
   return sh;
 }
 
