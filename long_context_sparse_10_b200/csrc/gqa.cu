@@ -72,6 +72,9 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kWgThreads = 128;
 constexpr int kStep = 64;  // keys of half a tile
 constexpr float kRescaleLog2 = 8.f;
+// A reference beyond this is subtracted from the scores themselves: the fused v * a - m * a is off by the rounding of
+// m * a, 2^-24 of it, which from 2^31 on would leave the range of the exponential.
+constexpr float kFarLog2 = 0x1p24f;
 
 // SINGLE: every item of the call fits one 128-row tile (decode), so one Q tile
 // is held and the space goes to more stages.
@@ -485,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       float m = -INFINITY, l = 0.f;
       bool any = false;  // a tile done
+      bool far = false;  // a row's reference is far out
       for (int j = w.t0; j < w.t1; ++j) {
         const int halves = steps_of(one, s, j, ks);
         if (halves == 0) continue;
@@ -518,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // complete, since these scores were issued after it
             const float f = need ? exp2_approx((m - mt) * sl2) : 1.f;
             if (need) m = mt;
+            far = __any_sync(0xffffffffu, m != -INFINITY && fabsf(m) * sl2 > kFarLog2);
             l *= f;
             if (any) {
 #pragma unroll 1
@@ -531,6 +536,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           ref = m == -INFINITY ? 0.f : -m * sl2;
+          if (far) {  // in TMEM, where they are read again: the way of ordinary rows stays as it is
+            const float at = m == -INFINITY ? 0.f : m;
+            ref = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < halves * kStep; c += 16) {
+              float x[16];
+              tmem_ld16(tS + c, x);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] -= at;
+              tmem_st16(tS + c, x);
+            }
+            tc::tmem_wait_st();
+          }
         }
         // keys past the sequence's end share its last tile: their values may be anything (another sequence,
         // a page never written), and 0 x NaN is NaN, so those rows of V become zeros.  The MMA warp, which

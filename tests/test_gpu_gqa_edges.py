@@ -263,3 +263,40 @@ def test_a_few_new_rows_a_sequence(lens, n, Hkv, G, dims):
     torch.cuda.synchronize()
     no_device_error()
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("top", [26, 31, 36, 64, 105])
+def test_scores_far_beyond_the_exponent_range(dims, top):
+    # scores of up to 2^top beside ordinary ones, row by row: a row is finite, one whose best key leads by more than fp32
+    # can err on two scores (and e^-100 weighs nothing) is that key's value, and ordinary rows are as ordinary as ever
+    L, G, scale = 700, 4, 0.09
+    g = np.random.default_rng(top)
+    power = g.integers(0, 2, (L, G)) * g.integers(0, top, (L, G)) * 1.0
+    q = (bf16(g, L, G, dims[0]).float() * torch.from_numpy(2.0**power)[..., None]).to(torch.bfloat16).to(DEV)
+    k, v = bf16(g, L, 1, dims[0]).to(DEV), bf16(g, L, 1, dims[1]).to(DEV)
+    ref, rl, mean, _ = attend64(q, k, v, scale)
+    size = scale * torch.einsum("thd,sd->ths", q.double().abs(), k[:, 0].double().abs()).amax(2)
+    err = (dims[0] + 8) * 2.0**-23 * size
+    x = scale * torch.einsum("thd,sd->ths", q.double(), k[:, 0].double())
+    x = x.masked_fill(torch.ones(L, L, dtype=torch.bool, device=DEV).triu(1)[:, None], -math.inf)
+    best = x.topk(2, 2).values
+    sure = f64(((best[..., 0] - best[..., 1]) > 2 * err + 100)).astype(bool)
+    near = power == 0  # scores as in every other test
+    assert int(sure.sum()) > 100 and int(near.sum()) > 100
+    table = np.arange(-(-L // 128))[None].astype(np.int32)
+    pad = lambda t: torch.cat([t, t[: table.size * 128 - L]]).view(table.size, 128, 1, -1).transpose(1, 2).contiguous()  # noqa: E731
+    cache = csa.GqaCache(pad(k), pad(v))
+    calls = {"prompt": (0, csa.gqa_dense_packed(q, k, v, csa.Packed([L], 1), scale))}
+    for n in (1, 3):  # the last rows as a decode step: their keys are shared out over several CTAs
+        batch = csa.GqaBatch(i32(table), i32([L]), i32([0, n]), max_q=n, total_q=n)
+        calls[f"last {n}"] = (L - n, csa.gqa_dense_paged(q[L - n:].contiguous(), cache, batch, scale))
+    no_device_error()
+    for what, (a, (out, lse)) in calls.items():
+        out, lse = f64(out), f64(lse)
+        assert bool(np.all(np.isfinite(out)) and np.all(np.isfinite(lse))), what
+        pick = sure[a:] | near[a:]
+        if pick.any():
+            check_out(out[pick], f64(ref)[a:][pick], f64(mean)[a:][pick], what)
+        worst = np.abs(lse - f64(rl)[a:]) / (f64(err)[a:] + 2.0**-18)
+        assert float(worst.max()) <= 1.0, what
