@@ -570,8 +570,10 @@ CSA_API size_t gqa_dense_workspace_size(int64_t max_q, int32_t H, int32_t H_kv, 
  *   last sequence are left as they were.  A score that is NaN or +inf (of a key
  *   that is not finite) shows as NaN in the row that sees it and in no other; a
  *   score of -inf weighs nothing, and a row that sees no other gets out = 0 and
- *   lse = -inf.  A sequence's own values must be finite: one that is not also
- *   reaches rows shortly before it (those that share its tile of 128 keys).
+ *   lse = -inf.  A sequence's own values must be finite, and below 2^96 (they are
+ *   summed with weights of up to 2^8 before the division): one that is not
+ *   finite also reaches rows shortly before it (those that share its tile of
+ *   128 keys).
  *   What another sequence holds never reaches it.
  */
 CSA_API csa_status gqa_dense_packed(const void* q, const void* k, const void* v, const csa_packed* packed, int32_t H,

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* empty = is_v ? &vempty[st] : &kempty[st];
         uint8_t* dst = is_v ? Vs + st * S::kVBytes : Ks + st * S::kQBytes;
         if (use > 0 && !wait_warp(empty, (use - 1) & 1)) return false;
-        if (lane == 0) bar_expect(full, static_cast<uint32_t>(is_v ? S::kVBytes : S::kQBytes));
+        if (lane == 0) tc::bar_arrive_expect_tx(full, static_cast<uint32_t>(is_v ? S::kVBytes : S::kQBytes));
         __syncwarp();
         if constexpr (PAGED) {
           // at most 3 column blocks x 8 pages: a lane each
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         const int nt = w.one ? 1 : 2;
         for (int s = 0; s < nt; ++s) {
-          bar_expect(&qfull[s], rows_q * 128u * S::kQc);
+          tc::bar_arrive_expect_tx(&qfull[s], rows_q * 128u * S::kQc);
           const int tok = w.q.row0 + w.blk * g.tpb + s * g.tpt;
           for (int c = 0; c < S::kQc; ++c)
             tc::tma_load_3d(Qs + s * S::kQBytes + c * (kTile * 128), &qmap, c * 64, w.h * g.G, tok, &qfull[s]);

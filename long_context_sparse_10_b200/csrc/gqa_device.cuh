@@ -180,7 +180,6 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* v, bool wi
     reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
 }
-__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) { tc::bar_arrive_expect_tx(bar, bytes); }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         healthy = wait_warp(&kempty[kr.st], kr.ph ^ 1u);
         if (!healthy) break;
-        if (lane == 0) bar_expect(&kfull[kr.st], S::kKBytes);
+        if (lane == 0) tc::bar_arrive_expect_tx(&kfull[kr.st], S::kKBytes);
         __syncwarp();
         if (c < S::kChunks)
           tc::tma_load_2d(Ks + kr.st * S::kKBytes + c * (kTile * 128) + pg * p.c.page * 128, &kmap, c * 64, row,
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         healthy = wait_warp(&qempty[qr.st], qr.ph ^ 1u);
         if (!healthy) break;
         if (lane == 0) {
-          bar_expect(&qfull[qr.st], static_cast<uint32_t>(g.tpt * g.G) * 128u * S::kChunks);
+          tc::bar_arrive_expect_tx(&qfull[qr.st], static_cast<uint32_t>(g.tpt * g.G) * 128u * S::kChunks);
           for (int c = 0; c < S::kChunks; ++c)
             tc::tma_load_3d(Qs + qr.st * q_bytes + c * p.cols * 128, &qmap, c * 64, w.h * g.G, w.q.row0 + b * g.tpb,
                             &qfull[qr.st]);
