@@ -39,14 +39,14 @@
 // operands.
 //
 // Measured (B200, 8192-token prompt, 32 query and 8 kv heads of 128 channels,
-// 550 GFLOP): 530 us in short runs at 1.9 GHz (0.63 of the measured bf16 peak),
-// 605 us in a sustained run at the power cap; the tensor pipe is active half the
-// time.  A 128-key tile takes a stream about 3900 clocks: 2400 of softmax (two
-// warps share a scheduler's exponential and fp32 units), 770 of MMAs, the rest
-// hand-overs: a barrier operation costs 100 to 250 clocks while the score MMAs
-// read both operands from shared memory at its full 128 bytes a clock.  Decode
-// (32 sequences of 1000 to 16384 tokens, 1.14 GB): 184 us, 0.95 of the measured
-// copy bandwidth; there the K/V stream is the bound.
+// 550 GFLOP): 601 us in a sustained run at the power cap (0.56 of the measured
+// bf16 peak); the tensor pipe is active half the time.  A 128-key tile takes a
+// stream about 3900 clocks: 2400 of softmax (two warps share a scheduler's
+// exponential and fp32 units), 770 of MMAs, the rest hand-overs: a barrier
+// operation costs 100 to 250 clocks while the score MMAs read both operands from
+// shared memory at its full 128 bytes a clock.  Decode (32 sequences of 1000 to
+// 16384 tokens, 1.14 GB): 189 to 201 us from GPU to GPU, 0.87 to 0.92 of the
+// measured copy bandwidth; there the K/V stream is the bound.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

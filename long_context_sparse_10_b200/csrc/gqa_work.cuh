@@ -51,7 +51,8 @@ struct Geometry {
 
 // sum_{t < n} floor((a t + b) / m) for a n + b < 2^32, in O(log) steps: whole
 // parts come out, and what is left is the same sum with the roles of the axes
-// exchanged (lattice points under the line).
+// exchanged: lattice points under a line, counted by the steps of the Euclidean
+// algorithm.
 CSA_HD int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
   int64_t ans = 0;
   while (n > 0) {
